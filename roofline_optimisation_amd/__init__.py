@@ -10,5 +10,6 @@ MI355X roofline.
 from .binding import (  # noqa: F401
     BF16, F16, F32, OK, VARIANTS, Gemm355Error, gemm355_kernel_desc, gemm355_run_variant,
     gemm355_select_variant, gemm355_status_string, gemm355_variant_name, gemm355_version,
-    gemm_bf16f32acc, gemm_f16f32acc, gemm_f32, lib, matmul,
+    gemm_bf16f32acc, gemm_f16f32acc, gemm_f32, lib, linear_cross_entropy,
+    linear_cross_entropy_grad, matmul, route, route_grad,
 )

@@ -42,8 +42,12 @@ EXPORTS = (
     "gemm355_probe_mfma_shape", "gemm355_probe_mfma", "gemm355_probe_ds_read_tr16",
     "gemm355_probe_global_load_lds", "gemm355_stream", "gemm355_chase",
     "gemm355_softmax_f32", "gemm355_row_sum_f32",
+    "gemm355_xent_workspace", "gemm355_xent", "gemm355_xent_grad_workspace", "gemm355_xent_grad",
+    "gemm355_route", "gemm355_route_grad",
 )
 
+ROUTE_SIGMOID, ROUTE_RENORM = 1, 2
+ROUTE_SCORES = {"softmax": 0, "sigmoid": ROUTE_SIGMOID}
 STREAM_COPY, STREAM_READ_XOR, STREAM_COPY_NT = 0, 1, 2
 
 
@@ -97,6 +101,18 @@ def _configure(lib):
     lib.gemm355_softmax_f32.restype = i
     lib.gemm355_row_sum_f32.argtypes = [i, i, p, i, p, p]
     lib.gemm355_row_sum_f32.restype = i
+    u, z, f = ctypes.c_uint, ctypes.c_size_t, ctypes.c_float
+    for name in ("gemm355_xent_workspace", "gemm355_xent_grad_workspace"):
+        getattr(lib, name).argtypes = [i, u, i, i, i]
+        getattr(lib, name).restype = z
+    lib.gemm355_xent.argtypes = [i, u, i, i, i, p, i, p, i, p, i64, p, p, p, z, p]
+    lib.gemm355_xent.restype = i
+    lib.gemm355_xent_grad.argtypes = [i, u, i, i, i, p, i, p, i, p, i64, p, p, p, i, p, i, p, z, p]
+    lib.gemm355_xent_grad.restype = i
+    lib.gemm355_route.argtypes = [i, u, i, i, i, i, i, i, p, i, p, f, p, p, p, p]
+    lib.gemm355_route.restype = i
+    lib.gemm355_route_grad.argtypes = [i, u, i, i, i, p, i, p, p, f, p, i, p]
+    lib.gemm355_route_grad.restype = i
     return lib
 
 
@@ -195,6 +211,38 @@ def gemm355_softmax_f32(rows, cols, X, ldx, Y, ldy, stream=0) -> int:
 
 def gemm355_row_sum_f32(rows, cols, X, ldx, out, stream=0) -> int:
     return lib().gemm355_row_sum_f32(rows, cols, X, ldx, out, stream)
+
+
+def gemm355_xent_workspace(dtype, flags, M, N, K) -> int:
+    return lib().gemm355_xent_workspace(dtype, flags, M, N, K)
+
+
+def gemm355_xent(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, lse, workspace,
+                 workspace_bytes, stream=0) -> int:
+    return lib().gemm355_xent(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, lse,
+                              workspace, workspace_bytes, stream)
+
+
+def gemm355_xent_grad_workspace(dtype, flags, M, N, K) -> int:
+    return lib().gemm355_xent_grad_workspace(dtype, flags, M, N, K)
+
+
+def gemm355_xent_grad(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, lse, dloss, dX, lddx,
+                      dW, lddw, workspace, workspace_bytes, stream=0) -> int:
+    return lib().gemm355_xent_grad(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, lse, dloss,
+                                   dX, lddx, dW, lddw, workspace, workspace_bytes, stream)
+
+
+def gemm355_route(dtype, flags, rows, experts, k, groups, top_groups, group_top, X, ldx, bias,
+                  scale, ids, weights, counts, stream=0) -> int:
+    return lib().gemm355_route(dtype, flags, rows, experts, k, groups, top_groups, group_top, X, ldx,
+                               bias, scale, ids, weights, counts, stream)
+
+
+def gemm355_route_grad(dtype, flags, rows, experts, k, X, ldx, ids, dweights, scale, dX, lddx,
+                       stream=0) -> int:
+    return lib().gemm355_route_grad(dtype, flags, rows, experts, k, X, ldx, ids, dweights, scale, dX,
+                                    lddx, stream)
 
 
 def status_string(status: int) -> str:
@@ -311,3 +359,198 @@ def row_sum(X, out=None, stream=None):
     if st != OK:
         raise Gemm355Error(st, "gemm355_row_sum_f32")
     return out
+
+
+class _on:
+    """What a call's allocations and launches need around them: the operands' device made
+    the current one, and, for a call on another stream than the current one, that stream (so
+    that the memory it allocates is that stream's, and is not handed out again before the
+    work on it is done).  Gives the stream's handle."""
+
+    def __init__(self, stream, device):
+        import torch
+        cuda = torch.cuda
+        self.contexts = []
+        if device.index is not None and device.index != cuda.current_device():
+            self.contexts.append(cuda.device(device))
+        current = cuda.current_stream(device).cuda_stream
+        if stream is None:
+            self.handle = current
+            return
+        self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if self.handle != current:
+            if not hasattr(stream, "cuda_stream"):
+                stream = cuda.ExternalStream(self.handle, device=device)
+            self.contexts.append(cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+_INT_MAX = 2 ** 31 - 1
+
+
+def _c_int(v, what) -> int:
+    """v as a C int; ctypes would cut a larger one short without a word."""
+    v = int(v)
+    if not -_INT_MAX - 1 <= v <= _INT_MAX:
+        raise ValueError(f"{what} does not fit a C int")
+    return v
+
+
+def _row_stride(t, what) -> int:
+    """The row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}'s rows must be contiguous (stride(1) == 1)")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{what}'s rows must not overlap (stride(0) >= columns)")
+    return _c_int(max(t.stride(0) if rows > 1 else cols, cols, 1), f"{what}'s row stride")
+
+
+def _vector(t, what, dtype, n, device):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on {device}")
+
+
+def _head_shapes(X, W, labels, trans_b):
+    """(dtype code, flags, M, N, K) of a projection X.op(W) with labels."""
+    import torch
+    if not (X.is_cuda and W.is_cuda) or X.device != W.device:
+        raise ValueError("X and W must be tensors on one CUDA device")
+    if X.dtype != W.dtype:
+        raise TypeError("X and W must have the same dtype")
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("expected 2-D tensors")
+    M, K = X.shape
+    K2, N = (W.shape[1], W.shape[0]) if trans_b else tuple(W.shape)
+    if K2 != K:
+        raise ValueError("inner dimensions differ")
+    _vector(labels, "labels", torch.int64, M, X.device)
+    for v in (M, N, K):
+        _c_int(v, "a dimension")
+    return _dtype_code(X), TRANS_B if trans_b else 0, M, N, K
+
+
+def _bytes(n, device):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def linear_cross_entropy(X, W, labels, *, trans_b: bool = False, ignore_index: int = -100, stream=None):
+    """(loss, lse), float32 per row, of the softmax cross entropy of the logits X.op(W)
+    through gemm355_xent, without the logits in memory: lse = log sum exp of a row's logits,
+    loss = lse - the label's logit, 0 where labels == ignore_index (NaN for another label
+    outside the vocabulary).  X is M x K, W is K x N, or N x K with trans_b (float32, float16
+    or bfloat16, rows contiguous); labels int64.  Raises Gemm355Error on a non-OK status."""
+    import torch
+    code, flags, M, N, K = _head_shapes(X, W, labels, trans_b)
+    if not -2 ** 63 <= ignore_index < 2 ** 63:
+        raise ValueError("ignore_index does not fit an int64")
+    with _on(stream, X.device) as handle:
+        out = torch.empty((2, M), dtype=torch.float32, device=X.device)
+        n = gemm355_xent_workspace(code, flags, M, N, K)
+        ws = _bytes(n, X.device)
+        loss, lse = out[0], out[1]
+        st = gemm355_xent(code, flags, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
+                          _row_stride(W, "W"), labels.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, handle)
+    if st != OK:
+        raise Gemm355Error(st, "gemm355_xent")
+    return loss, lse
+
+
+def linear_cross_entropy_grad(X, W, labels, lse, dloss, *, trans_b: bool = False, ignore_index: int = -100,
+                              need_dx: bool = True, need_dw: bool = True, stream=None):
+    """(dX, dW), in the operands' dtype, of sum(dloss * loss) for linear_cross_entropy's loss
+    through gemm355_xent_grad; lse as that call returned it, dloss float32 per row.  A
+    gradient that is not needed is None.  Raises Gemm355Error on a non-OK status."""
+    import torch
+    code, flags, M, N, K = _head_shapes(X, W, labels, trans_b)
+    if not -2 ** 63 <= ignore_index < 2 ** 63:
+        raise ValueError("ignore_index does not fit an int64")
+    _vector(lse, "lse", torch.float32, M, X.device)
+    _vector(dloss, "dloss", torch.float32, M, X.device)
+    with _on(stream, X.device) as handle:
+        dX = torch.empty((M, K), dtype=X.dtype, device=X.device) if need_dx else None
+        dW = torch.empty(tuple(W.shape), dtype=W.dtype, device=X.device) if need_dw else None
+        n = gemm355_xent_grad_workspace(code, flags, M, N, K)
+        ws = _bytes(n, X.device)
+        st = gemm355_xent_grad(code, flags, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
+                               _row_stride(W, "W"), labels.data_ptr(), ignore_index, lse.data_ptr(), dloss.data_ptr(),
+                               dX.data_ptr() if need_dx else 0, max(K, 1),
+                               dW.data_ptr() if need_dw else 0, max(int(W.shape[1]), 1), ws.data_ptr(), n,
+                               handle)
+    if st != OK:
+        raise Gemm355Error(st, "gemm355_xent_grad")
+    return dX, dW
+
+
+def _route_flags(score, renorm):
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score must be one of {sorted(ROUTE_SCORES)}")
+    return ROUTE_SCORES[score] | (ROUTE_RENORM if renorm else 0)
+
+
+def route(logits, k: int, *, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+          group_top: int = 1, renorm: bool = False, scale: float = 1.0, stream=None):
+    """(ids, weights, counts) of the k experts each row of router logits (rows x experts,
+    float32, float16 or bfloat16) goes to, through gemm355_route: ids int32 and weights
+    float32, rows x k, in falling order of softmax or sigmoid score plus bias (float32 per
+    expert, for the choice only) within the top_groups best of `groups` groups of experts;
+    counts int32 per expert.  Raises Gemm355Error on a non-OK status."""
+    import torch
+    flags = _route_flags(score, renorm)
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D CUDA tensor")
+    rows, experts = logits.shape
+    if bias is not None:
+        _vector(bias, "bias", torch.float32, experts, logits.device)
+    if not 1 <= k <= 64:
+        raise ValueError("k must be from 1 to 64")
+    for v, what in ((rows, "rows"), (experts, "experts"), (groups, "groups"), (top_groups, "top_groups"),
+                    (group_top, "group_top")):
+        _c_int(v, what)
+    with _on(stream, logits.device) as handle:
+        ids = torch.empty((rows, k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((rows, k), dtype=torch.float32, device=logits.device)
+        counts = torch.empty(experts, dtype=torch.int32, device=logits.device)
+        st = gemm355_route(_dtype_code(logits), flags, rows, experts, k, groups, top_groups, group_top,
+                           logits.data_ptr(), _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(), scale,
+                           ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), handle)
+    if st != OK:
+        raise Gemm355Error(st, "gemm355_route")
+    return ids, weights, counts
+
+
+def route_grad(logits, ids, dweights, *, score: str = "softmax", renorm: bool = False, scale: float = 1.0,
+               stream=None):
+    """The gradient to the logits (their dtype) of route's weights, for the experts `ids`
+    (int32, rows x k) and the weights' gradient dweights (float32, rows x k), through
+    gemm355_route_grad.  Raises Gemm355Error on a non-OK status."""
+    import torch
+    flags = _route_flags(score, renorm)
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D CUDA tensor")
+    rows, experts = logits.shape
+    for t, what, dtype in ((ids, "ids", torch.int32), (dweights, "dweights", torch.float32)):
+        if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.device != logits.device \
+                or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor of {rows} rows on {logits.device}")
+    if ids.shape != dweights.shape:
+        raise ValueError("ids and dweights must have the same shape")
+    for v, what in ((rows, "rows"), (experts, "experts"), (ids.shape[1], "k")):
+        _c_int(v, what)
+    with _on(stream, logits.device) as handle:
+        dx = torch.empty((rows, experts), dtype=logits.dtype, device=logits.device)
+        st = gemm355_route_grad(_dtype_code(logits), flags, rows, experts, int(ids.shape[1]), logits.data_ptr(),
+                                _row_stride(logits, "logits"), ids.data_ptr(), dweights.data_ptr(), scale, dx.data_ptr(),
+                                max(experts, 1), handle)
+    if st != OK:
+        raise Gemm355Error(st, "gemm355_route_grad")
+    return dx

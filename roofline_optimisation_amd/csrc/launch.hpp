@@ -36,4 +36,16 @@ inline bool rows_aligned16(const void *p, int ld, int elem_bytes) {
     return ((uintptr_t)p % 16 == 0) && (((size_t)ld * elem_bytes) % 16 == 0);
 }
 
+// A range of device addresses; an empty one meets nothing.
+struct Span {
+    uintptr_t a, b;
+    Span(const void *p, size_t bytes) : a((uintptr_t)p), b((uintptr_t)p + bytes) {}
+    bool meets(const Span &o) const { return a < b && o.a < o.b && a < o.b && o.a < b; }
+};
+
+// Bytes from the first to the last element of a rows x cols matrix of row stride ld.
+inline size_t matrix_bytes(int rows, int cols, int ld, size_t elem_bytes) {
+    return rows == 0 || cols == 0 ? 0 : ((size_t)(rows - 1) * ld + cols) * elem_bytes;
+}
+
 }  // namespace g355

@@ -362,26 +362,26 @@ def row_sum(X, out=None, stream=None):
 
 
 class _on:
-    """What a call's allocations and launches need around them: the operands' device made
-    the current one, and, for a call on another stream than the current one, that stream (so
-    that the memory it allocates is that stream's, and is not handed out again before the
-    work on it is done).  Gives the stream's handle."""
+    """A call on another stream than the current one, or on another device: that device and
+    stream are made the current ones around its allocations and launches (the memory it
+    allocates is then that stream's, and is not handed out again before the work on it is
+    done).  Without either, nothing is entered."""
 
     def __init__(self, stream, device):
         import torch
         cuda = torch.cuda
-        self.contexts = []
-        if device.index is not None and device.index != cuda.current_device():
-            self.contexts.append(cuda.device(device))
-        current = cuda.current_stream(device).cuda_stream
-        if stream is None:
-            self.handle = current
-            return
-        self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if self.handle != current:
-            if not hasattr(stream, "cuda_stream"):
-                stream = cuda.ExternalStream(self.handle, device=device)
-            self.contexts.append(cuda.stream(stream))
+        self.contexts = ()
+        index = device.index
+        self.handle = torch._C._cuda_getCurrentRawStream(index)
+        if index != cuda.current_device():
+            self.contexts = (cuda.device(device),)
+        if stream is not None:
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            if handle != self.handle:
+                self.handle = handle
+                if not hasattr(stream, "cuda_stream"):
+                    stream = cuda.ExternalStream(handle, device=device)
+                self.contexts += (cuda.stream(stream),)
 
     def __enter__(self):
         for c in self.contexts:
@@ -396,22 +396,27 @@ class _on:
 _INT_MAX = 2 ** 31 - 1
 
 
-def _c_int(v, what) -> int:
-    """v as a C int; ctypes would cut a larger one short without a word."""
-    v = int(v)
-    if not -_INT_MAX - 1 <= v <= _INT_MAX:
-        raise ValueError(f"{what} does not fit a C int")
-    return v
+def _c_ints(*values) -> None:
+    """Refuses what does not fit a C int: ctypes would cut it short without a word."""
+    for v in values:
+        if not -_INT_MAX - 1 <= v <= _INT_MAX:
+            raise ValueError(f"{v} does not fit a C int")
 
 
 def _row_stride(t, what) -> int:
     """The row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}'s rows must be contiguous (stride(1) == 1)")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{what}'s rows must not overlap (stride(0) >= columns)")
-    return _c_int(max(t.stride(0) if rows > 1 else cols, cols, 1), f"{what}'s row stride")
+    if rows > 1:
+        if ld < cols:
+            raise ValueError(f"{what}'s rows must not overlap (stride(0) >= columns)")
+    else:
+        ld = cols
+    if ld > _INT_MAX:
+        raise ValueError(f"{what}'s row stride does not fit a C int")
+    return ld or 1
 
 
 def _vector(t, what, dtype, n, device):
@@ -433,14 +438,8 @@ def _head_shapes(X, W, labels, trans_b):
     if K2 != K:
         raise ValueError("inner dimensions differ")
     _vector(labels, "labels", torch.int64, M, X.device)
-    for v in (M, N, K):
-        _c_int(v, "a dimension")
+    _c_ints(M, N, K)
     return _dtype_code(X), TRANS_B if trans_b else 0, M, N, K
-
-
-def _bytes(n, device):
-    import torch
-    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def linear_cross_entropy(X, W, labels, *, trans_b: bool = False, ignore_index: int = -100, stream=None):
@@ -454,10 +453,9 @@ def linear_cross_entropy(X, W, labels, *, trans_b: bool = False, ignore_index: i
     if not -2 ** 63 <= ignore_index < 2 ** 63:
         raise ValueError("ignore_index does not fit an int64")
     with _on(stream, X.device) as handle:
-        out = torch.empty((2, M), dtype=torch.float32, device=X.device)
+        loss, lse = X.new_empty(M, dtype=torch.float32), X.new_empty(M, dtype=torch.float32)
         n = gemm355_xent_workspace(code, flags, M, N, K)
-        ws = _bytes(n, X.device)
-        loss, lse = out[0], out[1]
+        ws = X.new_empty(n, dtype=torch.uint8)
         st = gemm355_xent(code, flags, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
                           _row_stride(W, "W"), labels.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, handle)
     if st != OK:
@@ -477,10 +475,10 @@ def linear_cross_entropy_grad(X, W, labels, lse, dloss, *, trans_b: bool = False
     _vector(lse, "lse", torch.float32, M, X.device)
     _vector(dloss, "dloss", torch.float32, M, X.device)
     with _on(stream, X.device) as handle:
-        dX = torch.empty((M, K), dtype=X.dtype, device=X.device) if need_dx else None
-        dW = torch.empty(tuple(W.shape), dtype=W.dtype, device=X.device) if need_dw else None
+        dX = X.new_empty((M, K)) if need_dx else None
+        dW = W.new_empty(W.shape) if need_dw else None
         n = gemm355_xent_grad_workspace(code, flags, M, N, K)
-        ws = _bytes(n, X.device)
+        ws = X.new_empty(n, dtype=torch.uint8)
         st = gemm355_xent_grad(code, flags, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
                                _row_stride(W, "W"), labels.data_ptr(), ignore_index, lse.data_ptr(), dloss.data_ptr(),
                                dX.data_ptr() if need_dx else 0, max(K, 1),
@@ -513,13 +511,11 @@ def route(logits, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
         _vector(bias, "bias", torch.float32, experts, logits.device)
     if not 1 <= k <= 64:
         raise ValueError("k must be from 1 to 64")
-    for v, what in ((rows, "rows"), (experts, "experts"), (groups, "groups"), (top_groups, "top_groups"),
-                    (group_top, "group_top")):
-        _c_int(v, what)
+    _c_ints(rows, experts, groups, top_groups, group_top)
     with _on(stream, logits.device) as handle:
-        ids = torch.empty((rows, k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((rows, k), dtype=torch.float32, device=logits.device)
-        counts = torch.empty(experts, dtype=torch.int32, device=logits.device)
+        ids = logits.new_empty((rows, k), dtype=torch.int32)
+        weights = logits.new_empty((rows, k), dtype=torch.float32)
+        counts = logits.new_empty(experts, dtype=torch.int32)
         st = gemm355_route(_dtype_code(logits), flags, rows, experts, k, groups, top_groups, group_top,
                            logits.data_ptr(), _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(), scale,
                            ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), handle)
@@ -544,10 +540,9 @@ def route_grad(logits, ids, dweights, *, score: str = "softmax", renorm: bool = 
             raise ValueError(f"{what} must be a contiguous {dtype} tensor of {rows} rows on {logits.device}")
     if ids.shape != dweights.shape:
         raise ValueError("ids and dweights must have the same shape")
-    for v, what in ((rows, "rows"), (experts, "experts"), (ids.shape[1], "k")):
-        _c_int(v, what)
+    _c_ints(rows, experts, ids.shape[1])
     with _on(stream, logits.device) as handle:
-        dx = torch.empty((rows, experts), dtype=logits.dtype, device=logits.device)
+        dx = logits.new_empty((rows, experts))
         st = gemm355_route_grad(_dtype_code(logits), flags, rows, experts, int(ids.shape[1]), logits.data_ptr(),
                                 _row_stride(logits, "logits"), ids.data_ptr(), dweights.data_ptr(), scale, dx.data_ptr(),
                                 max(experts, 1), handle)

@@ -472,16 +472,22 @@ __device__ __forceinline__ void store_tile(floatx4 (&acc)[kMB][kNB], float *__re
     }
 }
 
+// The epilogue of the plain GEMM kernels: store_tile.
+struct StoreEpilogue {};
+
 // WHOLE: the caller guarantees that the tile lies inside M x N (no guarded stores).
 // KR: K is not a whole number of ring trips (K a multiple of 8): the loop runs to the next
 // whole trip, every chunk at k >= K loads as zeros (DmaOp::issue), and the k-steps of the
 // last trip that lie wholly at k >= K are skipped.
+// EX: what becomes of the wave's accumulators: store_tile, or a functor of its own that is
+// called as ex.apply<EDGE>(acc, row0, col0), the wave's first row and column, with EDGE where
+// the tile reaches past ex.rows() or ex.cols() (M and N then only bound the loads).
 template <typename T, bool A_MN, bool B_MN, int EPI, int EM, int EN, int WM, int WN, int NS, int PW,
-          bool WHOLE = false, bool KR = false>
+          bool WHOLE = false, bool KR = false, class EX = StoreEpilogue>
 __device__ __forceinline__ void dma_tile(int M, int N, int K, const uint16_t *__restrict__ A, int lda,
                                          const uint16_t *__restrict__ B, int ldb,
                                          float *__restrict__ C, int ldc, float sign,
-                                         int flags, int m0, int n0, char *lds_raw) {
+                                         int flags, int m0, int n0, char *lds_raw, const EX &ex = EX()) {
     // the producer waves run every k-step's barrier; they do not skip the tail's steps
     static_assert(!(KR && PW > 0), "K past whole ring trips needs the compute waves to load");
     using G = Geo<EM, EN, WM, WN, NS, PW>;
@@ -705,7 +711,12 @@ __device__ __forceinline__ void dma_tile(int M, int N, int K, const uint16_t *__
     pin_acc(acc);
     asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
     pin_acc(acc);
-    if (WHOLE || (m0 + EM <= M && n0 + EN <= N))
+    if constexpr (!std::is_same<EX, StoreEpilogue>::value) {
+        if (m0 + EM <= ex.rows() && n0 + EN <= ex.cols())
+            ex.template apply<false>(acc, m0 + wm * G::kTM, n0 + wn * G::kTN);
+        else
+            ex.template apply<true>(acc, m0 + wm * G::kTM, n0 + wn * G::kTN);
+    } else if (WHOLE || (m0 + EM <= M && n0 + EN <= N))
         store_tile<EPI, T, false>(acc, C, ldc, m0 + wm * G::kTM, n0 + wn * G::kTN, M, N, sign, flags);
     else
         store_tile<EPI, T, true>(acc, C, ldc, m0 + wm * G::kTM, n0 + wn * G::kTN, M, N, sign, flags);

@@ -14,6 +14,7 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "wave_reduce.hpp"
+#include "xent.hpp"
 
 namespace g355 {
 
@@ -24,10 +25,6 @@ constexpr int kMaxDim = (1 << 30) - 1;
 
 // A row's running statistics: maximum m, sum l of exp(z - m), the label's logit.
 struct RowState { float m, l, z; };
-
-// What the gradient needs of a row: its log-sum-exp, the upstream gradient (scaled) and the
-// label, -1 for a row without one (whose g is 0 and whose copy of X is 0).
-struct RowGrad { float lse, g; int label, unused; };
 
 // (m, l) merged with another pair; an empty pair is (-infinity, 0).
 __device__ __forceinline__ void merge_pair(float &m, float &l, float mo, float lo) {
@@ -98,13 +95,58 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(int nc, int v0, int N, c
     else finish_row(row, s.m, s.l, s.z, label, ignore, N, loss, lse);
 }
 
+// The statistics of the fused tiles: `blocks` pairs per row (part[block * ldp + row]) merged,
+// and the row's results written.  A workgroup takes R rows, 1024 / R threads a row: each
+// merges every (1024 / R)-th block, then the threads' pairs are merged in halves.
+template <int R>
+__global__ __launch_bounds__(1024) void xent_merge_kernel(int M, int N, int blocks, const float2 *__restrict__ part,
+                                                          int ldp, const float *__restrict__ zl,
+                                                          const int64_t *__restrict__ labels, int64_t ignore,
+                                                          float *loss, float *lse) {
+    constexpr int kPer = 1024 / R;
+    __shared__ float sm[1024], sl[1024];
+    const int t = threadIdx.x, row = blockIdx.x * R + t % R;
+    float m = kNegInf, l = 0.0f;
+    if (row < M)
+        for (int b = t / R; b < blocks; b += 4 * kPer) {
+            float2 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                v[u] = b + u * kPer < blocks ? part[(size_t)(b + u * kPer) * ldp + row] : make_float2(kNegInf, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) merge_pair(m, l, v[u].x, v[u].y);
+        }
+    sm[t] = m;
+    sl[t] = l;
+#pragma unroll
+    for (int h = 512; h >= R; h /= 2) {
+        __syncthreads();
+        if (t < h) {
+            merge_pair(m, l, sm[t + h], sl[t + h]);
+            sm[t] = m;
+            sl[t] = l;
+        }
+    }
+    if (t >= R || row >= M) return;
+    const int64_t label = labels[row];
+    finish_row(row, m, l, label >= 0 && label < N ? zl[row] : 0.0f, label, ignore, N, loss, lse);
+}
+
+// X's rows copied to rows of ldm elements, zeros after the K-th.
+__global__ __launch_bounds__(256) void xent_copy_kernel(int K, const uint16_t *__restrict__ X, int ldx, uint16_t *Xm,
+                                                        int ldm) {
+    for (int c = threadIdx.x; c < ldm; c += 256)
+        Xm[(size_t)blockIdx.x * ldm + c] = c < K ? X[(size_t)blockIdx.x * ldx + c] : (uint16_t)0;
+}
+
 // Before the gradient's pieces: scale[0] = S and scale[1] = 1 / S (S = 1 unless `rescale`:
 // then the power of two that puts the largest |dloss| in [2^13, 2^14), from 2^-100 to
 // 2^100), the rows' RowGrad, and Xm = X with the rows without a label set to zero (their
 // products with a zero row of dZ would not be zero where X holds an infinity or NaN).
 // Every workgroup finds the same maximum over all rows, then does its share of the rows.
+// Rows from M to Mp are rows without a label.
 template <typename E>
-__global__ __launch_bounds__(256) void xent_prep_kernel(int M, int N, int K, const E *__restrict__ X, int ldx,
+__global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int N, int K, const E *__restrict__ X, int ldx,
                                                         const int64_t *__restrict__ labels, int64_t ignore,
                                                         const float *__restrict__ lse,
                                                         const float *__restrict__ dloss, int rescale,
@@ -128,9 +170,9 @@ __global__ __launch_bounds__(256) void xent_prep_kernel(int M, int N, int K, con
         scale[0] = S;
         scale[1] = 1.0f / S;
     }
-    for (int r = blockIdx.x; r < M; r += gridDim.x) {
-        const int64_t y = labels[r];
-        const bool live = y != ignore && y >= 0 && y < N;
+    for (int r = blockIdx.x; r < Mp; r += gridDim.x) {
+        const int64_t y = r < M ? labels[r] : -1;
+        const bool live = r < M && y != ignore && y >= 0 && y < N;
         if (threadIdx.x == 0)
             rows[r] = live ? RowGrad{lse[r], dloss[r] * S, (int)y, 0} : RowGrad{0.0f, 0.0f, -1, 0};
         const E *x = X + (size_t)r * ldx;
@@ -157,9 +199,11 @@ __global__ __launch_bounds__(256) void xent_dz_kernel(int nc, int v0, const floa
     }
 }
 
-// out = scale[1] * acc, rounded to the 16-bit type.  Grid: (columns / 1024, rows).
+// out = scale[1] * (the sum of `splits` partial sums, `stride` apart), rounded to the 16-bit
+// type.  Grid: (columns / 1024, rows).
 template <typename T>
 __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *__restrict__ acc, int lda,
+                                                         int splits, size_t stride,
                                                          const float *__restrict__ scale, uint16_t *out,
                                                          int ldo) {
     const float f = scale[1];
@@ -167,7 +211,10 @@ __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *
     for (int u = 0; u < 4; ++u) {
         const int c = blockIdx.x * 1024 + 256 * u + (int)threadIdx.x;
         if (c >= cols) break;
-        out[(size_t)blockIdx.y * ldo + c] = to_bits(f * acc[(size_t)blockIdx.y * lda + c], T{});
+        const float *a = acc + (size_t)blockIdx.y * lda + c;
+        float v = a[0];
+        for (int i = 1; i < splits; ++i) v += a[i * stride];
+        out[(size_t)blockIdx.y * ldo + c] = to_bits(f * v, T{});
     }
 }
 
@@ -252,6 +299,87 @@ struct GradPlan {
     }
 };
 
+// Whether the matrix-core tiles with fused epilogues take these shapes: 16-bit types, K a
+// multiple of 8 of at least one ring trip, and more classes than one tile has.
+bool fused_shape(int dtype, unsigned flags, int N, int K) {
+    return dtype != kF32 && K % 8 == 0 && K >= 128 && N >= 256 && (flags & GEMM355_TRANS_B || N % 8 == 0);
+}
+
+// Byte offsets of `rows` rows of stride ld (and the ring trip past them) below 2^31.
+bool offsets_fit(long rows, long ld) { return (rows + 256) * ld * 2 < (1L << 31); }
+
+// Whether W's rows can be loaded by them: 16-byte aligned, and offsets within a tile (TRANS_B)
+// or of all K rows in range.
+bool fused_weights(unsigned flags, int K, const void *W, int ldw) {
+    return rows_aligned16(W, ldw, 2) && offsets_fit(flags & GEMM355_TRANS_B ? 256 : K, ldw);
+}
+
+// Rows of the tile (EM x 256) for M rows.
+int tile_rows(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+constexpr int kStatRows = 32768;  // rows whose block statistics are held at once
+
+struct FusedForwardPlan {
+    int rows, em, blocks, ldm;
+    float2 *part;
+    float *zl;
+    uint16_t *Xm;
+    size_t bytes;
+    FusedForwardPlan(int M, int N, int K, void *ws) {
+        rows = M < kStatRows ? M : kStatRows;
+        em = tile_rows(rows);
+        blocks = cdiv(N, 256) * (256 / stat_cols(em));
+        ldm = K;
+        Carver c{(char *)ws};
+        part = (float2 *)c.take((size_t)blocks * rows * sizeof(float2));
+        zl = (float *)c.take((size_t)rows * 4);
+        Xm = (uint16_t *)c.take((size_t)rows * ldm * 2);
+        bytes = c.used;
+    }
+};
+
+// The ranges of K one product is split into: `want` of them at most, each a whole number of
+// ring trips and none but a single one shorter than 256.
+struct Splits {
+    int count, step;
+    Splits(int K, int want) {
+        if (want > K / 512) want = K / 512;
+        if (want < 1) want = 1;
+        step = (int)up((size_t)cdiv(K, want), 128);
+        while (step < K && K % step != 0 && K % step < 256) step += 128;
+        count = cdiv(K, step);
+    }
+};
+
+constexpr long kDzBytes = 1L << 29;  // dZ of a piece
+
+struct FusedGradPlan {
+    int cols, Mp, ldm, em, splits;
+    float *scale, *dX;
+    RowGrad *rows;
+    uint16_t *Xm, *dZ;
+    size_t bytes;
+    FusedGradPlan(int M, int N, int K, void *ws) {
+        Mp = (int)up((size_t)M, 128);  // whole ring trips of dW's product, zeros past M
+        ldm = K;
+        em = tile_rows(M);
+        const long fit = kDzBytes / 2 / Mp / 256 * 256;
+        const int pieces = (int)((N + (fit < 256 ? 256 : fit) - 1) / (fit < 256 ? 256 : fit));
+        cols = (int)up((size_t)cdiv(N, pieces), 256);
+        while (cols < N && N % cols != 0 && N % cols < 256) cols += 256;
+        // dX's product: as many ranges of a piece's classes as fill the 256 CUs
+        const int nc = cols < N ? cols : N;
+        splits = Splits(nc, 256 / (cdiv(M, em) * cdiv(K, 256))).count;
+        Carver c{(char *)ws};
+        scale = (float *)c.take(8);
+        rows = (RowGrad *)c.take((size_t)Mp * sizeof(RowGrad));
+        Xm = (uint16_t *)c.take((size_t)Mp * ldm * 2);
+        dZ = (uint16_t *)c.take((size_t)Mp * cols * 2);
+        dX = (float *)c.take((size_t)splits * M * K * 4);
+        bytes = c.used;
+    }
+};
+
 bool valid_shape(int dtype, unsigned flags, int M, int N, int K) {
     if (dtype < kF32 || dtype > kBF16 || (flags & ~(unsigned)GEMM355_TRANS_B)) return false;
     if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return false;
@@ -276,6 +404,43 @@ size_t w_offset(unsigned flags, int v0, int ldw) {
 
 gemm355_status status_of(hipError_t e) { return e == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH; }
 
+#define G355_TRY(call)                                    \
+    do {                                                  \
+        const hipError_t try_e = (call);                  \
+        if (try_e != hipSuccess) return GEMM355_ERR_LAUNCH; \
+    } while (0)
+
+hipError_t merge(int M, int N, const FusedForwardPlan &p, const int64_t *labels, int64_t ignore, float *loss,
+                 float *lse, hipStream_t s) {
+    if (M >= 32)
+        hipLaunchKernelGGL((xent_merge_kernel<32>), dim3(cdiv(M, 32)), dim3(1024), 0, s, M, N, p.blocks, p.part,
+                           p.rows, p.zl, labels, ignore, loss, lse);
+    else
+        hipLaunchKernelGGL((xent_merge_kernel<4>), dim3(cdiv(M, 4)), dim3(1024), 0, s, M, N, p.blocks, p.part,
+                           p.rows, p.zl, labels, ignore, loss, lse);
+    return hipGetLastError();
+}
+
+gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
+                             int ldw, const int64_t *labels, int64_t ignore, float *loss, float *lse, void *ws,
+                             hipStream_t s) {
+    const FusedForwardPlan p(M, N, K, ws);
+    const bool copy = !rows_aligned16(X, ldx, 2) || !offsets_fit(256, ldx);
+    for (int r0 = 0; r0 < M; r0 += p.rows) {
+        const int rows = M - r0 < p.rows ? M - r0 : p.rows;
+        const void *x = at(X, (size_t)r0 * ldx, 2);
+        if (copy) {
+            hipLaunchKernelGGL(xent_copy_kernel, dim3(rows), dim3(256), 0, s, K, (const uint16_t *)x, ldx, p.Xm, p.ldm);
+            G355_TRY(hipGetLastError());
+        }
+        const HeadArgs h{rows, N, K, copy ? p.Xm : x, copy ? p.ldm : ldx, W, ldw, (flags & GEMM355_TRANS_B) != 0};
+        G355_TRY(dtype == kF16 ? launch_xent_stats_f16(p.em, h, labels + r0, p.part, p.rows, p.zl, s)
+                               : launch_xent_stats_bf16(p.em, h, labels + r0, p.part, p.rows, p.zl, s));
+        G355_TRY(merge(rows, N, p, labels + r0, ignore, loss ? loss + r0 : nullptr, lse ? lse + r0 : nullptr, s));
+    }
+    return GEMM355_OK;
+}
+
 gemm355_status forward(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
                        int ldw, const int64_t *labels, int64_t ignore, float *loss, float *lse, void *ws,
                        hipStream_t s) {
@@ -298,7 +463,6 @@ gemm355_status forward(int dtype, unsigned flags, int M, int N, int K, const voi
     return GEMM355_OK;
 }
 
-// The rows' kernels of the gradient for one storage type.
 struct GradCall {
     int dtype;
     unsigned flags;
@@ -317,15 +481,15 @@ struct GradCall {
     hipStream_t s;
 };
 
-hipError_t prep(const GradCall &a, const GradPlan &p) {
-    const dim3 grid(a.M < 1024 ? a.M : 1024);
+hipError_t prep(const GradCall &a, int Mp, float *scale, RowGrad *rows, void *Xm, int ldm) {
+    const dim3 grid(Mp < 1024 ? Mp : 1024);
     if (a.dtype == kF32)
-        hipLaunchKernelGGL((xent_prep_kernel<float>), grid, dim3(256), 0, a.s, a.M, a.N, a.K, (const float *)a.X,
-                           a.ldx, a.labels, a.ignore, a.lse, a.dloss, 0, p.scale, p.rows, (float *)p.Xm, p.ldm);
+        hipLaunchKernelGGL((xent_prep_kernel<float>), grid, dim3(256), 0, a.s, a.M, Mp, a.N, a.K, (const float *)a.X,
+                           a.ldx, a.labels, a.ignore, a.lse, a.dloss, 0, scale, rows, (float *)Xm, ldm);
     else
-        hipLaunchKernelGGL((xent_prep_kernel<uint16_t>), grid, dim3(256), 0, a.s, a.M, a.N, a.K,
+        hipLaunchKernelGGL((xent_prep_kernel<uint16_t>), grid, dim3(256), 0, a.s, a.M, Mp, a.N, a.K,
                            (const uint16_t *)a.X, a.ldx, a.labels, a.ignore, a.lse, a.dloss,
-                           a.dtype == kF16 ? 1 : 0, p.scale, p.rows, (uint16_t *)p.Xm, p.ldm);
+                           a.dtype == kF16 ? 1 : 0, scale, rows, (uint16_t *)Xm, ldm);
     return hipGetLastError();
 }
 
@@ -345,24 +509,91 @@ hipError_t piece_dz(const GradCall &a, const GradPlan &p, int v0, int nc) {
     });
 }
 
-hipError_t round16(const GradCall &a, const GradPlan &p, int rows, int cols, const float *acc, int lda, void *out,
-                   int ldo) {
+hipError_t round16(const GradCall &a, int rows, int cols, const float *acc, int lda, int splits, size_t stride,
+                   const float *scale, void *out, int ldo) {
     return over_rows(rows, [&](int r, int n) {
         const dim3 grid(cdiv(cols, 1024), n);
         if (a.dtype == kF16)
             hipLaunchKernelGGL((xent_round_kernel<f16_t>), grid, dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda,
-                               p.scale, (uint16_t *)out + (size_t)r * ldo, ldo);
+                               splits, stride, scale, (uint16_t *)out + (size_t)r * ldo, ldo);
         else
             hipLaunchKernelGGL((xent_round_kernel<bf16_t>), grid, dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda,
-                               p.scale, (uint16_t *)out + (size_t)r * ldo, ldo);
+                               splits, stride, scale, (uint16_t *)out + (size_t)r * ldo, ldo);
     });
+}
+
+gemm355_status gradient_fused(const GradCall &a, void *ws) {
+    const FusedGradPlan p(a.M, a.N, a.K, ws);
+    const bool tb = a.flags & GEMM355_TRANS_B, f16 = a.dtype == kF16;
+    G355_TRY(prep(a, p.Mp, p.scale, p.rows, p.Xm, p.ldm));
+    const bool one = p.cols >= a.N && p.splits == 1;  // dX in one product
+    for (int v0 = 0; v0 < a.N; v0 += p.cols) {
+        const int nc = a.N - v0 < p.cols ? a.N - v0 : p.cols;
+        const auto *w = (const uint16_t *)at(a.W, w_offset(a.flags, v0, a.ldw), 2);
+        const HeadArgs h{p.Mp, nc, a.K, p.Xm, p.ldm, w, a.ldw, tb};
+        G355_TRY(f16 ? launch_xent_dz_f16(p.em, h, p.rows, v0, p.dZ, p.cols, a.s)
+                     : launch_xent_dz_bf16(p.em, h, p.rows, v0, p.dZ, p.cols, a.s));
+        if (a.dX != nullptr) {
+            const Splits sp(nc, p.splits);
+            ProductArgs q{};
+            q.M = q.rows = a.M;
+            q.N = q.cols = a.K;
+            q.K = nc;
+            q.A = p.dZ;
+            q.lda = p.cols;
+            q.B = w;
+            q.ldb = a.ldw;
+            q.splits = sp.count;
+            q.step = sp.step;
+            if (one) {
+                q.out = (uint16_t *)a.dX;
+                q.ldo = a.lddx;
+                q.factor = p.scale + 1;
+            } else {
+                q.part = p.dX;
+                q.part_stride = (size_t)a.M * a.K;
+                q.ldo = a.K;
+                q.accumulate = v0 > 0;
+            }
+            G355_TRY(f16 ? launch_xent_dx_f16(p.em, tb, q, a.s) : launch_xent_dx_bf16(p.em, tb, q, a.s));
+        }
+        if (a.dW != nullptr) {
+            ProductArgs q{};
+            const int padded = (int)up((size_t)nc, 8);
+            q.K = p.Mp;
+            q.A = tb ? p.dZ : p.Xm;
+            q.lda = tb ? p.cols : p.ldm;
+            q.B = tb ? p.Xm : p.dZ;
+            q.ldb = tb ? p.ldm : p.cols;
+            q.M = tb ? padded : a.K;
+            q.N = tb ? a.K : padded;
+            q.rows = tb ? nc : a.K;
+            q.cols = tb ? a.K : nc;
+            q.out = (uint16_t *)at(a.dW, w_offset(a.flags, v0, a.lddw), 2);
+            q.ldo = a.lddw;
+            q.factor = p.scale + 1;
+            const int tile = (long)cdiv(q.rows, 256) * cdiv(q.cols, 256) >= 256 ? 256 : 128;
+            G355_TRY(f16 ? launch_xent_dw_f16(tile, q, a.s) : launch_xent_dw_bf16(tile, q, a.s));
+        }
+    }
+    if (!one && a.dX != nullptr)
+        G355_TRY(round16(a, a.M, a.K, p.dX, a.K, p.splits, (size_t)a.M * a.K, p.scale, a.dX, a.lddx));
+    return GEMM355_OK;
+}
+
+// Whether the fused gradient takes this call: every operand's offsets in range.
+bool fused_gradient(const GradCall &a) {
+    if (!fused_shape(a.dtype, a.flags, a.N, a.K) || !fused_weights(a.flags, a.K, a.W, a.ldw)) return false;
+    const FusedGradPlan p(a.M, a.N, a.K, nullptr);
+    return offsets_fit(p.Mp, p.cols) && offsets_fit(p.Mp, p.ldm) &&
+           (!(a.flags & GEMM355_TRANS_B) || offsets_fit(p.cols, a.ldw));
 }
 
 gemm355_status gradient(const GradCall &a, void *ws) {
     const GradPlan p(a.dtype, a.M, a.N, a.K, ws);
     const bool h16 = a.dtype != kF32, tb = a.flags & GEMM355_TRANS_B;
     const size_t es = h16 ? 2 : 4;
-    hipError_t e = prep(a, p);
+    hipError_t e = prep(a, a.M, p.scale, p.rows, p.Xm, p.ldm);
     if (e != hipSuccess) return status_of(e);
     float *dx = h16 ? p.dX : (float *)a.dX;
     const int lddx = h16 ? a.K : a.lddx;
@@ -392,12 +623,12 @@ gemm355_status gradient(const GradCall &a, void *ws) {
                                       p.dZ, p.cols, out, ldo, a.s);
             if (st != GEMM355_OK) return st;
             if (h16) {
-                e = round16(a, p, rows, cols, out, ldo, dw, a.lddw);
+                e = round16(a, rows, cols, out, ldo, 1, 0, p.scale, dw, a.lddw);
                 if (e != hipSuccess) return status_of(e);
             }
         }
     }
-    if (h16 && a.dX != nullptr) return status_of(round16(a, p, a.M, a.K, p.dX, a.K, a.dX, a.lddx));
+    if (h16 && a.dX != nullptr) return status_of(round16(a, a.M, a.K, p.dX, a.K, 1, 0, p.scale, a.dX, a.lddx));
     return GEMM355_OK;
 }
 
@@ -411,7 +642,10 @@ extern "C" {
 
 size_t gemm355_xent_workspace(int dtype, unsigned flags, int M, int N, int K) {
     if (!valid_shape(dtype, flags, M, N, K) || M == 0) return 0;
-    return ForwardPlan(M, N, nullptr).bytes;
+    const size_t any = ForwardPlan(M, N, nullptr).bytes;
+    if (!fused_shape(dtype, flags, N, K)) return any;
+    const size_t fused = FusedForwardPlan(M, N, K, nullptr).bytes;
+    return fused > any ? fused : any;  // which one runs depends on W's alignment
 }
 
 gemm355_status gemm355_xent(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
@@ -436,12 +670,17 @@ gemm355_status gemm355_xent(int dtype, unsigned flags, int M, int N, int K, cons
             if (out[i].meets(out[j])) return GEMM355_ERR_INVALID_ARG;
     }
     if (!current_device_is_gfx950()) return GEMM355_ERR_DEVICE;
-    return forward(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, lse, workspace, stream);
+    const bool fused = fused_shape(dtype, flags, N, K) && fused_weights(flags, K, W, ldw);
+    return (fused ? forward_fused : forward)(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, lse,
+                                             workspace, stream);
 }
 
 size_t gemm355_xent_grad_workspace(int dtype, unsigned flags, int M, int N, int K) {
     if (!valid_shape(dtype, flags, M, N, K) || M == 0) return 0;
-    return GradPlan(dtype, M, N, K, nullptr).bytes;
+    const size_t any = GradPlan(dtype, M, N, K, nullptr).bytes;
+    if (!fused_shape(dtype, flags, N, K)) return any;
+    const size_t fused = FusedGradPlan(M, N, K, nullptr).bytes;
+    return fused > any ? fused : any;
 }
 
 gemm355_status gemm355_xent_grad(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx,
@@ -488,7 +727,7 @@ gemm355_status gemm355_xent_grad(int dtype, unsigned flags, int M, int N, int K,
                                    (uint16_t *)dW + (size_t)r * lddw, lddw);
         }));
     const GradCall a{dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, lse, dloss, dX, lddx, dW, lddw, stream};
-    return gradient(a, workspace);
+    return fused_gradient(a) ? gradient_fused(a, workspace) : gradient(a, workspace);
 }
 
 }  // extern "C"

@@ -1,0 +1,14 @@
+// The products of bfloat16 dZ with the head and with the hidden rows (xent_dma.hpp).
+#include "xent_dma.hpp"
+
+namespace g355 {
+
+hipError_t launch_xent_dx_bf16(int em, bool b_mn, const ProductArgs &p, hipStream_t s) {
+    return launch_dx<bf16_t>(em, b_mn, p, s);
+}
+
+hipError_t launch_xent_dw_bf16(int tile, const ProductArgs &p, hipStream_t s) {
+    return launch_dw<bf16_t>(tile, p, s);
+}
+
+}  // namespace g355

@@ -1,0 +1,73 @@
+// What the softmax cross entropy's files share: a row's data for the gradient, and the
+// matrix-core launches of the 16-bit types (xent_dma.hpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "common.hpp"
+
+namespace g355 {
+
+// What the gradient needs of a row: its log-sum-exp, the upstream gradient (scaled) and the
+// label, -1 for a row without one (whose lse and g are 0 and whose copy of X is 0).
+struct RowGrad { float lse, g; int label, unused; };
+
+// Z = X.op(W) of M rows and N classes; with trans_b W holds a class per row.  Rows start on
+// 16-byte boundaries, K is a multiple of 8 and at least 128, and a K x N W has N a multiple
+// of 8.
+struct HeadArgs {
+    int M, N, K;
+    const void *X;
+    int ldx;
+    const void *W;
+    int ldw;
+    bool trans_b;
+};
+
+// Statistics of Z by blocks of stat_cols(em) columns: part[block * ldp + row] = (maximum,
+// sum of exp(z - maximum)) and, where a row's label falls into Z, zl[row] = its logit.
+// em: the tile's rows, 64, 128 or 256.
+constexpr int stat_cols(int em) { return em == 64 ? 64 : 128; }
+hipError_t launch_xent_stats_f16(int em, const HeadArgs &h, const int64_t *labels, float2 *part, int ldp,
+                                 float *zl, hipStream_t s);
+hipError_t launch_xent_stats_bf16(int em, const HeadArgs &h, const int64_t *labels, float2 *part, int ldp,
+                                  float *zl, hipStream_t s);
+
+// dZ (M x N rounded up to a multiple of 8, row stride ldz, the added columns 0) of the
+// classes v0 .. v0 + N, W pointing at the first of them.
+hipError_t launch_xent_dz_f16(int em, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
+                              hipStream_t s);
+hipError_t launch_xent_dz_bf16(int em, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
+                               hipStream_t s);
+
+// A product of the gradient: op(A).op(B) over K.  A is M x K (k-contiguous), or K x M with
+// a_mn; B is N x K, or K x N with b_mn.  M and N bound the loads (multiples of 8 where the
+// operand is m/n-contiguous); rows x cols of the result are stored.
+struct ProductArgs {
+    int M, N, K;
+    const uint16_t *A;
+    int lda;
+    const uint16_t *B;
+    int ldb;
+    int rows, cols;
+    // 16-bit result: out = round(*factor * product)
+    uint16_t *out;
+    int ldo;
+    const float *factor;
+    // or binary32 partial sums: K walked in `splits` ranges of `step`, range r's sums at
+    // part + r * part_stride, row stride ldo, added to what is there when `accumulate`
+    float *part;
+    size_t part_stride;
+    int splits, step, accumulate;
+};
+
+// dX's product: A = dZ (k-contiguous), B m/n-contiguous or not; partial sums, or the 16-bit
+// result when p.part is NULL.  em x 256 tiles, em = 64, 128 or 256.
+hipError_t launch_xent_dx_f16(int em, bool b_mn, const ProductArgs &p, hipStream_t s);
+hipError_t launch_xent_dx_bf16(int em, bool b_mn, const ProductArgs &p, hipStream_t s);
+// dW's product: both operands m/n-contiguous, K a multiple of 128, 16-bit result.  Square
+// tiles of extent 128 or 256.
+hipError_t launch_xent_dw_f16(int tile, const ProductArgs &p, hipStream_t s);
+hipError_t launch_xent_dw_bf16(int tile, const ProductArgs &p, hipStream_t s);
+
+}  // namespace g355

@@ -1,0 +1,315 @@
+// The softmax cross entropy's products for the 16-bit types: the direct-to-LDS tile routine
+// (h16_dma.hpp) with epilogues that turn a tile of logits into row statistics, or into dZ,
+// in the registers the tile was summed in.
+#pragma once
+
+#include "h16_gemm.hpp"
+#include "wave_reduce.hpp"
+#include "xent.hpp"
+
+namespace g355 {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Maximum and sum over the 16 lanes that hold a row of a 16 x 16 accumulator quad; every
+// one of them gets the result.
+__device__ __forceinline__ float row16_max(float v) {
+    v = fmaxf(v, DppXchg<kDppQuadXor1>::get(v));
+    v = fmaxf(v, DppXchg<kDppQuadXor2>::get(v));
+    v = fmaxf(v, DppXchg<kDppRowHalfMirror>::get(v));
+    return fmaxf(v, DppXchg<kDppRowMirror>::get(v));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+    v += DppXchg<kDppQuadXor1>::get(v);
+    v += DppXchg<kDppQuadXor2>::get(v);
+    v += DppXchg<kDppRowHalfMirror>::get(v);
+    return v + DppXchg<kDppRowMirror>::get(v);
+}
+
+// An accumulator register, read where it is used (left to itself the compiler copies all 256
+// of a 256 x 256 tile out of the accumulator file at once, which does not fit).
+__device__ __forceinline__ float acc_read(float v) {
+    float a;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(a) : "a"(v));
+    return a;
+}
+
+// Row statistics of the wave's tile.  Quad (i, j) holds rows row0 + 16 i + 4 (l/16) + r,
+// columns col0 + 16 j + l%16: a row's values are kNB registers of 16 lanes.  Per row the
+// maximum over registers and lanes, then the sum of exponentials.  Of every 16 results of a
+// lane's 4 quad rows, lane l%16 = c keeps the one of quad row c / 4, register c % 4, so that
+// 64 consecutive rows leave in one store.
+struct StatsEpilogue {
+    int M, N;
+    const int64_t *labels;
+    float2 *part;
+    int ldp;
+    float *zl;
+    __device__ int rows() const { return M; }
+    __device__ int cols() const { return N; }
+
+    template <bool EDGE, int kMB, int kNB>
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+        const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4;
+        float2 *const out = part + (size_t)(col0 / (16 * kNB)) * ldp;
+        constexpr float kNegInf = -__builtin_huge_valf();
+#pragma unroll
+        for (int g = 0; g < kMB; g += 4) {
+            constexpr int kI = kMB < 4 ? kMB : 4;
+            float km = kNegInf, kl = 0.0f;
+#pragma unroll
+            for (int ii = 0; ii < kI; ++ii) {
+                const int i = g + ii, r0 = row0 + 16 * i + 4 * q4;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = r0 + r;
+                    float x[kNB];
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j) {
+                        x[j] = acc_read(acc[i][j][r]);
+                        if (EDGE && col0 + 16 * j + c16 >= N) x[j] = kNegInf;
+                    }
+                    // the label's logit, where its column is in this tile (of a row of many
+                    // columns few tiles hold any)
+                    const int64_t rel = (!EDGE || row < M) ? labels[row] - col0 : -1;
+                    const bool hit = rel >= 0 && rel < 16 * kNB;
+                    if (__any(hit)) {
+#pragma unroll
+                        for (int j = 0; j < kNB; ++j)
+                            if (hit && (int)rel == 16 * j + c16 && (!EDGE || col0 + (int)rel < N)) zl[row] = x[j];
+                    }
+                    float m = x[0];
+#pragma unroll
+                    for (int j = 1; j < kNB; ++j) m = fmaxf(m, x[j]);
+                    m = row16_max(m);
+                    const float shift = m == kNegInf ? 0.0f : m;
+                    float l = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j) l += __builtin_amdgcn_exp2f((x[j] - shift) * kLog2e);
+                    l = row16_sum(l);
+                    if (c16 == 4 * ii + r) {
+                        km = m;
+                        kl = l;
+                    }
+                }
+            }
+            const int row = row0 + 16 * (g + (c16 >> 2)) + 4 * q4 + (c16 & 3);
+            if (c16 < 4 * kI && (!EDGE || row < M)) out[row] = make_float2(km, kl);
+        }
+    }
+};
+
+// One row of a pair of quads as 4-byte words of two 16-bit values: lanes 2m and 2m + 1
+// exchange a register, the even lane gets columns 2m, 2m + 1 of the first quad, the odd lane
+// those of the second.
+template <typename T>
+__device__ __forceinline__ uint32_t pair_word(float a0, float a1, int odd) {
+    const float other = DppXchg<kDppQuadXor1>::get(odd ? a0 : a1);
+    const float lo = odd ? other : a0, hi = odd ? a1 : other;
+    return (uint32_t)to_bits(lo, T{}) | ((uint32_t)to_bits(hi, T{}) << 16);
+}
+
+// dZ of the wave's tile: g (exp(z - lse) - [column is the label]), rounded to T.  Columns
+// from N to the next multiple of 8 are written as 0.
+template <typename T>
+struct DzEpilogue {
+    int M, N, v0;
+    const RowGrad *rg;
+    uint16_t *out;
+    int ldo;
+    __device__ int rows() const { return M; }
+    __device__ int cols() const { return N; }
+
+    template <bool EDGE, int kMB, int kNB>
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+        const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4, odd = lane & 1;
+        const int cw = col0 + (lane & 14) + 16 * odd, padded = (N + 7) & ~7;
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = row0 + 16 * i + 4 * q4 + r;
+                RowGrad w{0.0f, 0.0f, -1, 0};
+                if (!EDGE || row < M) w = rg[row];
+                const int hot = w.label - v0 - col0 - c16;
+                float d[kNB];
+#pragma unroll
+                for (int j = 0; j < kNB; ++j) {
+                    const float p = __builtin_amdgcn_exp2f((acc_read(acc[i][j][r]) - w.lse) * kLog2e);
+                    d[j] = fmaf(w.g, p, hot == 16 * j ? -w.g : 0.0f);
+                    if (EDGE && col0 + 16 * j + c16 >= N) d[j] = 0.0f;
+                }
+                uint16_t *o = out + (size_t)row * ldo + cw;
+#pragma unroll
+                for (int j = 0; j < kNB; j += 2) {
+                    const uint32_t v = pair_word<T>(d[j], d[j + 1], odd);
+                    if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(o + 16 * j) = v;
+                }
+            }
+    }
+};
+
+// The 16-bit result of a product: round(factor * sum), in 4-byte words where the output
+// allows them.
+template <typename T>
+struct RoundEpilogue {
+    int nrows, ncols;
+    uint16_t *out;
+    int ldo, words;
+    const float *factor;
+    __device__ int rows() const { return nrows; }
+    __device__ int cols() const { return ncols; }
+
+    template <bool EDGE, int kMB, int kNB>
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+        const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4, odd = lane & 1;
+        const float f = *factor;
+        const int cw = words ? col0 + (lane & 14) + 16 * odd : col0 + c16;
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = row0 + 16 * i + 4 * q4 + r;
+                uint16_t *o = out + (size_t)row * ldo + cw;
+#pragma unroll
+                for (int j = 0; j < kNB; j += 2) {
+                    const float a0 = f * acc_read(acc[i][j][r]), a1 = f * acc_read(acc[i][j + 1][r]);
+                    if (words) {
+                        const uint32_t v = pair_word<T>(a0, a1, odd);
+                        if (!EDGE || (row < nrows && cw + 16 * j + 1 < ncols)) *(uint32_t *)(o + 16 * j) = v;
+                        else if (row < nrows && cw + 16 * j < ncols) o[16 * j] = (uint16_t)v;
+                    } else {
+                        if (!EDGE || (row < nrows && cw + 16 * j < ncols)) o[16 * j] = to_bits(a0, T{});
+                        if (!EDGE || (row < nrows && cw + 16 * j + 16 < ncols)) o[16 * j + 16] = to_bits(a1, T{});
+                    }
+                }
+            }
+    }
+};
+
+// EM x 256 tiles: 256 rows on 2 x 2 waves of 128 x 128, 128 rows on 2 x 2 of 64 x 128, 64
+// rows on 1 x 4 of 64 x 64; a 4-stage ring.
+template <int EM>
+struct HeadTile {
+    static constexpr int kWM = EM == 64 ? 1 : 2, kWN = EM == 64 ? 4 : 2, kNs = 4;
+    using G = dma::Geo<EM, 256, kWM, kWN, kNs, 0>;
+};
+
+template <typename T, bool W_MN, int EM, bool KR, class EX>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EM == 64 ? 2 : 1)))
+void xent_head_kernel(int M, int N, int K, const uint16_t *__restrict__ X, int ldx,
+                      const uint16_t *__restrict__ W, int ldw, EX ex) {
+    using H = HeadTile<EM>;
+    __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
+    int tm, tn;
+    grouped_tile(xcd_contiguous_id(blockIdx.x, gridDim.x), cdiv(M, EM), cdiv(N, 256), 4, tm, tn);
+    dma::dma_tile<T, false, W_MN, 0, EM, 256, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
+        M, N, K, X, ldx, W, ldw, nullptr, 0, 1.0f, 0, tm * EM, tn * 256, lds, ex);
+}
+
+// dX's product over one of p.splits ranges of K: partial sums (EPI 0 or, adding to what is
+// there, 1), or the rounded result.
+template <typename T, bool B_MN, int EM, bool KR, int EPI>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EM == 64 ? 2 : 1)))
+void xent_dx_kernel(ProductArgs p, int words) {
+    using H = HeadTile<EM>;
+    __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
+    const int tiles = cdiv(p.M, EM) * cdiv(p.N, 256);
+    const int id = xcd_contiguous_id(blockIdx.x, gridDim.x);
+    const int split = id / tiles;
+    int tm, tn;
+    grouped_tile(id - split * tiles, cdiv(p.M, EM), cdiv(p.N, 256), 4, tm, tn);
+    const int k0 = split * p.step;
+    const int K = split + 1 < p.splits ? p.step : p.K - k0;
+    const uint16_t *A = p.A + k0, *B = p.B + (B_MN ? (size_t)k0 * p.ldb : (size_t)k0);
+    if constexpr (EPI < 2) {
+        dma::dma_tile<T, false, B_MN, EPI, EM, 256, H::kWM, H::kWN, H::kNs, 0, false, KR>(
+            p.rows, p.cols, K, A, p.lda, B, p.ldb, p.part + split * p.part_stride, p.ldo, 1.0f, EPI, tm * EM,
+            tn * 256, lds);
+    } else {
+        using EX = RoundEpilogue<T>;
+        dma::dma_tile<T, false, B_MN, 0, EM, 256, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
+            p.M, p.N, K, A, p.lda, B, p.ldb, nullptr, 0, 1.0f, 0, tm * EM, tn * 256, lds,
+            EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
+    }
+}
+
+template <typename T, int E>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(E == 128 ? 2 : 1)))
+void xent_dw_kernel(ProductArgs p, int words) {
+    using G = dma::Geo<E, E, 2, 2, 4, 0>;
+    using EX = RoundEpilogue<T>;
+    __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
+    int tm, tn;
+    grouped_tile(xcd_contiguous_id(blockIdx.x, gridDim.x), cdiv(p.rows, E), cdiv(p.cols, E), 4, tm, tn);
+    dma::dma_tile<T, true, true, 0, E, E, 2, 2, 4, 0, false, false, EX>(
+        p.M, p.N, p.K, p.A, p.lda, p.B, p.ldb, nullptr, 0, 1.0f, 0, tm * E, tn * E, lds,
+        EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
+}
+
+template <typename T, bool W_MN, int EM, class EX>
+hipError_t launch_head_tile(const HeadArgs &h, const EX &ex, hipStream_t s) {
+    const dim3 grid(cdiv(h.M, EM) * cdiv(h.N, 256));
+    const auto *X = (const uint16_t *)h.X, *W = (const uint16_t *)h.W;
+    if (h.K % 128 != 0)
+        hipLaunchKernelGGL((xent_head_kernel<T, W_MN, EM, true, EX>), grid, dim3(256), 0, s, h.M, h.N, h.K, X,
+                           h.ldx, W, h.ldw, ex);
+    else
+        hipLaunchKernelGGL((xent_head_kernel<T, W_MN, EM, false, EX>), grid, dim3(256), 0, s, h.M, h.N, h.K, X,
+                           h.ldx, W, h.ldw, ex);
+    return hipGetLastError();
+}
+
+template <typename T, class EX>
+hipError_t launch_head(int em, const HeadArgs &h, const EX &ex, hipStream_t s) {
+    if (h.trans_b) {
+        if (em == 64) return launch_head_tile<T, false, 64>(h, ex, s);
+        if (em == 128) return launch_head_tile<T, false, 128>(h, ex, s);
+        return launch_head_tile<T, false, 256>(h, ex, s);
+    }
+    if (em == 64) return launch_head_tile<T, true, 64>(h, ex, s);
+    if (em == 128) return launch_head_tile<T, true, 128>(h, ex, s);
+    return launch_head_tile<T, true, 256>(h, ex, s);
+}
+
+inline int word_stores(const ProductArgs &p) { return p.ldo % 2 == 0 && (uintptr_t)p.out % 4 == 0; }
+
+template <typename T, bool B_MN, int EM, bool KR>
+hipError_t launch_dx_epi(const ProductArgs &p, hipStream_t s) {
+    const dim3 grid(cdiv(p.M, EM) * cdiv(p.N, 256) * p.splits);
+    if (p.part == nullptr)
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, EM, KR, 2>), grid, dim3(256), 0, s, p, word_stores(p));
+    else if (p.accumulate)
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, EM, KR, 1>), grid, dim3(256), 0, s, p, 0);
+    else
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, EM, KR, 0>), grid, dim3(256), 0, s, p, 0);
+    return hipGetLastError();
+}
+
+template <typename T, bool B_MN>
+hipError_t launch_dx_layout(int em, const ProductArgs &p, hipStream_t s) {
+    // the ranges before the last are whole ring trips
+    const bool kr = p.K % 128 != 0;
+    if (em == 64) return kr ? launch_dx_epi<T, B_MN, 64, true>(p, s) : launch_dx_epi<T, B_MN, 64, false>(p, s);
+    if (em == 128) return kr ? launch_dx_epi<T, B_MN, 128, true>(p, s) : launch_dx_epi<T, B_MN, 128, false>(p, s);
+    return kr ? launch_dx_epi<T, B_MN, 256, true>(p, s) : launch_dx_epi<T, B_MN, 256, false>(p, s);
+}
+
+template <typename T>
+hipError_t launch_dx(int em, bool b_mn, const ProductArgs &p, hipStream_t s) {
+    return b_mn ? launch_dx_layout<T, true>(em, p, s) : launch_dx_layout<T, false>(em, p, s);
+}
+
+template <typename T>
+hipError_t launch_dw(int tile, const ProductArgs &p, hipStream_t s) {
+    const dim3 grid(cdiv(p.rows, tile) * cdiv(p.cols, tile));
+    if (tile == 128) hipLaunchKernelGGL((xent_dw_kernel<T, 128>), grid, dim3(256), 0, s, p, word_stores(p));
+    else hipLaunchKernelGGL((xent_dw_kernel<T, 256>), grid, dim3(256), 0, s, p, word_stores(p));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace g355

@@ -124,7 +124,7 @@ def test_wrappers_refuse():
     with pytest.raises(ValueError):
         gb._row_stride(torch.zeros(8, 4).t(), "X")              # columns first
     with pytest.raises(ValueError):
-        gb._c_int(1 << 31, "M")
+        gb._c_ints(3, 1 << 31)
     assert gb._row_stride(torch.zeros(4, 10)[:, :8], "X") == 10
     assert gb._row_stride(torch.zeros(8, 1).t(), "X") == 8
     assert gb._row_stride(torch.zeros(4, 0), "X") == 1

@@ -139,8 +139,9 @@ enum {
  *     ids = the k kept experts of the largest c_e, in falling order
  *     weights_i = scale * s[ids_i]             (GEMM355_ROUTE_RENORM: / sum_j s[ids_j])
  *
- * Ties go to the lowest index.  Scores and choices are computed in binary64, so the ids
- * do not depend on the rounding of the scores; weights are rounded once to binary32.
+ * Ties go to the lowest index.  Where binary32 scores cannot tell two choices or two group
+ * scores apart they are compared in binary64; without a bias experts are compared by their
+ * logits.  Weights are computed in binary64 and rounded once to binary32.
  * counts[e] (experts values; NULL when not wanted) is the number of rows that chose e.
  *
  * An expert whose logit is -infinity, or whose bias is -infinity or NaN, is masked: it is

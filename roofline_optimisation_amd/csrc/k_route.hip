@@ -3,9 +3,17 @@
 //
 // The row softmax is the one of "Kernel optimisation guide" (section on softmax
 // optimisation); the choice adds a bias, keeps the best groups and takes the k best, ties
-// to the lowest index.  Scores are computed in binary64: the ids are whole numbers, and two
-// choices that differ by less than a binary32 rounding would otherwise be ordered by the
-// order of a sum.
+// to the lowest index.
+//
+// One wave takes a row, Q = experts / 64 of its experts per lane.  A row is a few hundred
+// bytes, so the time goes into instructions, not memory.  The ids are whole numbers and have
+// to be those of exact scores, but only rows with two candidates closer than binary32 can
+// tell apart need better: a row is first decided on 32-bit keys (the logits themselves where
+// no bias is added, so exactly; else binary32 scores plus bias), and where two neighbours of
+// the resulting order, or two groups, are closer than the bound of the scores' error, the
+// row is decided again on binary64 scores.  Each round takes the largest key (a maximum over
+// registers, four register exchanges within 16 lanes, a scalar maximum of four lanes) and
+// the lowest expert that holds it (a ballot per register).
 #include "../../include/gemm355_softmax.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -54,120 +62,348 @@ __global__ void zero_counts_kernel(int n, int32_t *counts) {
     if (i < n) counts[i] = 0;
 }
 
-// One wave per row, Q experts per lane (expert q * 64 + lane), four rows per workgroup.
+// Binary32 in an order-preserving 32-bit form; 0 is below every value's.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);  // -0 as +0
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+    return __builtin_bit_cast(float, k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// The wave's largest v, as a scalar.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max(v, dpp_u32<kDppQuadXor1>(v));
+    v = max(v, dpp_u32<kDppQuadXor2>(v));
+    v = max(v, dpp_u32<kDppRowHalfMirror>(v));
+    v = max(v, dpp_u32<kDppRowMirror>(v));
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+__device__ __forceinline__ float wave_max(float v) { return of_key(wave_max_u32(key_of(v))); }
+
+// Which of the groups' scores (one per lane) are among the `top` largest, ties to the lowest
+// group; `near`: two scores lie within `margin` of each other.
+template <typename F>
+__device__ __forceinline__ unsigned long long best_groups(F score, int groups, int top, F margin, bool &near) {
+    const int lane = threadIdx.x % 64;
+    int rank = 0;
+    bool close = false;
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+        const F o = __shfl(score, g, 64);
+        rank += o > score || (o == score && g < lane);
+        close |= g != lane && o - score <= margin && score - o <= margin;
+    }
+    near = __any(close && lane < groups);
+    return __ballot(lane < groups && rank < top);
+}
+
+// A group's score from the choices of its experts (in the wave's LDS row, `per` of them).
+template <typename F>
+__device__ __forceinline__ F group_score(const F *choice, int per, int group_top) {
+    const F low = (F)kLow;
+    F best = low, second = low;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) {
+        const F v = choice[i];
+        second = fmax(second, fmin(best, v));
+        best = fmax(best, v);
+    }
+    return group_top == 2 && second > low ? best + second : best;
+}
+
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// exp in binary64: x = n log 2 + r with |r| <= log 2 / 2 (log 2 in two parts, the first short
+// enough for n times it to be exact), the Taylor sum of exp(r) to r^13 / 13! (the next term
+// is below 2^-57), times 2^n.  The coefficients 1 / 13!, 1 / 12!, ... 1 lie in LDS: held in
+// registers across a kernel's loop over rows they take 28 scalar ones.
+constexpr int kTaylor = 14;
+__device__ __forceinline__ void taylor_to_lds(double *coef) {
+    if (threadIdx.x < kTaylor) {
+        double f = 1.0;
+        for (int i = kTaylor - 1 - (int)threadIdx.x; i > 1; --i) f *= (double)i;
+        coef[threadIdx.x] = 1.0 / f;
+    }
+}
+__device__ __forceinline__ double exp64(double x, const double *coef) {
+    x = fmin(fmax(x, -1000.0), 1000.0);
+    const double n = rint(x * 1.4426950408889634074);
+    double r = fma(n, -0x1.62e42fefap-1, x);
+    r = fma(n, -0x1.cf79abc9e3b3ap-40, r);
+    double p = coef[0];
+#pragma unroll
+    for (int i = 1; i < kTaylor; ++i) p = fma(p, r, coef[i]);
+    return ldexp(p, (int)n);
+}
+
+// The score of a logit in binary64, for softmax before the division by the row's sum.
+template <bool SIGMOID>
+__device__ __forceinline__ double score64(float x, float m, const double *coef) {
+    const bool masked = !(x > -__builtin_huge_valf());
+    const double d = masked ? 0.0 : (double)x - (SIGMOID ? 0.0 : (double)m);
+    const double v = exp64(SIGMOID ? -d : d, coef);
+    return masked ? 0.0 : SIGMOID ? 1.0 / (1.0 + v) : v;
+}
+
+// A row's logit, -infinity past its experts.
+template <typename T>
+__device__ __forceinline__ float logit_at(const void *X, size_t x0, int e, int experts) {
+    const float x = load_elem<T>(X, x0 + min(e, experts - 1));
+    return e < experts ? x : -__builtin_huge_valf();
+}
+
+// The row's ids by binary64 scores: id of place i in lane i.  x: the row's logits, choice:
+// the wave's row of LDS, of which a lane touches its own experts only, but for the groups'
+// scores.  Rows that come here are few, so this keeps to few registers.
 template <typename T, int Q, bool SIGMOID>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a, bool renorm) {
-    __shared__ double choice_lds[4][Q * 64];
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    const int row = blockIdx.x * 4 + wave;
-    const bool live = row < a.rows;   // every wave stays for the barrier
-    double s[Q], c[Q];
-    bool bad = false;
-    float m = -__builtin_huge_valf();
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int e = q * 64 + lane;
-        const float x = live && e < a.experts ? load_elem<T>(a.X, (size_t)row * a.ldx + e)
-                                              : -__builtin_huge_valf();
-        bad |= x != x || (!SIGMOID && x == __builtin_huge_valf());
-        m = fmaxf(m, x);
-        s[q] = (double)x;
+__device__ __forceinline__ int exact_ids(const RouteArgs &a, const void *X, size_t x0, float m, double *choice,
+                                         const double *coef) {
+    const int lane = threadIdx.x % 64;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const double v = score64<SIGMOID>(logit_at<T>(X, x0, e0 + lane, a.experts), m, coef);
+        choice[e0 + lane] = v;
+        sum += v;
     }
-    bad = __any(bad);
-    if constexpr (SIGMOID) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            c[q] = s[q];
-            s[q] = 1.0 / (1.0 + exp(-s[q]));
-        }
-    } else {
-        for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
-        double sum = 0.0;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            c[q] = s[q];
-            s[q] = s[q] == kLow ? 0.0 : exp(s[q] - (double)m);
-            sum += s[q];
-        }
-        sum = wave_sum64(sum);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) s[q] = sum > 0.0 ? s[q] / sum : 0.0;
+    sum = SIGMOID ? 1.0 : wave_sum64(sum);
+#pragma unroll 1
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int e = e0 + lane;
+        const float b = a.bias != nullptr ? a.bias[min(e, a.experts - 1)] : 0.0f;
+        const double c = choice[e] / sum + (double)b;
+        const bool in = logit_at<T>(X, x0, e, a.experts) > -__builtin_huge_valf() && c > kLow;
+        choice[e] = in ? c : kLow;   // masked, absent, NaN bias
     }
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int e = q * 64 + lane;
-        const double v = s[q] + (a.bias != nullptr && e < a.experts ? (double)a.bias[e] : 0.0);
-        c[q] = c[q] > kLow && v > kLow ? v : kLow;   // masked, absent and NaN choices
-    }
+    unsigned long long kept = ~0ull;
+    const int per = a.experts / a.groups;
     if (a.top_groups < a.groups) {
-        const int per = a.experts / a.groups;
+        wave_lds_sync();
+        const double own = group_score(choice + min(lane, a.groups - 1) * per, per, a.group_top);
+        const double score = lane < a.groups ? own : kLow;
+        wave_lds_sync();
+        bool near;
+        kept = best_groups(score, a.groups, a.top_groups, 0.0, near);
+    }
+#pragma unroll 1
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int e = e0 + lane;
+        double c = choice[e];
+        // without a bias the order within the kept groups is the logits'
+        if (a.bias == nullptr && c > kLow) c = (double)logit_at<T>(X, x0, e, a.experts);
+        choice[e] = (kept >> ((e / per) & 63)) & 1 ? c : kLow;
+    }
+    int id = -1;
+#pragma unroll 1
+    for (int i = 0; i < a.k; ++i) {
+        double v = kLow;
+        int at = 0x7fffffff;
+#pragma unroll 1
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const double c = choice[e0 + lane];
+            at = c > v ? e0 + lane : at;
+            v = fmax(c, v);
+        }
+#pragma unroll 1
+        for (int d = 1; d < 64; d *= 2) {
+            const double vo = shfl_xor64(v, d);
+            const int ao = __shfl_xor(at, d, 64);
+            const bool theirs = vo > v || (vo == v && ao < at);
+            v = theirs ? vo : v;
+            at = theirs ? ao : at;
+        }
+        at = __builtin_amdgcn_readfirstlane(at);
+        if (at == 0x7fffffff) break;   // no expert left
+        id = lane == i ? at : id;
+        if (at % 64 == lane) choice[at] = kLow;
+    }
+    return id;
+}
+
+// With 8 experts per lane or more, keeps one expert's lane masks (two scalar registers each) from
+// being formed before the last one's are used.
+template <int Q>
+__device__ __forceinline__ void few_masks() {
+    if constexpr (Q >= 8) __builtin_amdgcn_sched_barrier(0);
+}
+
+// Rows of more than 512 experts are always decided on binary64 scores: 16 keys and their lane
+// masks per lane do not fit the scalar registers.
+constexpr bool has_keys(int Q) { return Q <= 8; }
+
+constexpr int kRouteWaves = 8;
+constexpr int kRouteGrid = 1024;  // workgroups; each takes every kRouteGrid-th group of rows
+
+// BIAS: choices add a.bias.  GROUPS: a.top_groups < a.groups.  SINGLE: one workgroup takes
+// every row, and writes the counts; else they are added to.
+template <typename T, int Q, bool SIGMOID, bool BIAS, bool GROUPS>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bool renorm, bool single) {
+    constexpr bool kExact = BIAS || GROUPS || !has_keys(Q);
+    __shared__ double choice_lds[kExact ? kRouteWaves : 1][kExact ? Q * 64 : 1];
+    __shared__ int hist[Q * 64];
+    __shared__ double coef[kTaylor];
+    const int wave = threadIdx.x / 64, lane0 = threadIdx.x % 64;
+    constexpr float kNegInf = -__builtin_huge_valf();
+    const bool count = a.counts != nullptr;
+    taylor_to_lds(coef);
+    if (count)
+        for (int e = threadIdx.x; e < a.experts; e += 64 * kRouteWaves) hist[e] = 0;
+    __syncthreads();
+    float b[Q], top_b = 0.0f;
+    if constexpr (BIAS && has_keys(Q)) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) choice_lds[wave][q * 64 + lane] = c[q];
-        __syncthreads();
-        double best = kLow, second = kLow;
-        if (lane < a.groups)
-            for (int i = 0; i < per; ++i) {
-                const double v = choice_lds[wave][lane * per + i];
-                if (v > best) {
-                    second = best;
-                    best = v;
-                } else if (v > second) {
-                    second = v;
+        for (int q = 0; q < Q; ++q) {
+            const int e = q * 64 + lane0;
+            b[q] = e < a.experts ? a.bias[e] : 0.0f;
+            // a masked expert's bias bounds nothing (NaN: the maximum ignores it)
+            top_b = fmaxf(top_b, b[q] == kNegInf ? 0.0f : fabsf(b[q]));
+        }
+        top_b = wave_max(top_b);
+    }
+    for (int row = blockIdx.x * kRouteWaves + wave; row < a.rows; row += gridDim.x * kRouteWaves) {
+        // the lane as each row's own value, or the masks of absent experts, two scalar registers
+        // each, are kept across rows
+        int lane = lane0;
+        asm volatile("" : "+v"(lane));
+        float x[Q], m = kNegInf;
+        bool bad = false;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            x[q] = logit_at<T>(a.X, (size_t)row * a.ldx, q * 64 + lane, a.experts);
+            bad |= x[q] != x[q] || (!SIGMOID && x[q] == __builtin_huge_valf());
+            m = fmaxf(m, x[q]);
+        }
+        bad = __any(bad);
+        m = wave_max(m);
+        int id = -1;
+        if (!bad && m > kNegInf) {
+            bool near = true;
+            if constexpr (has_keys(Q)) {
+                // binary32 scores s, each within 2^-24 (1 + (E / 64 + 32) s) of the exact one: a
+                // score's relative error is at most 2^-24 (2 |x| + 8), for softmax 2^-24 (2 |x - m|
+                // + E / 64 + 32) with the sum's, and 2 d exp(-d) < 1
+                uint32_t key[Q];
+                float s[Q];
+                float margin = 0.0f;
+                if constexpr (BIAS || GROUPS) {
+                    float largest = 1.0f;
+                    if constexpr (SIGMOID) {
+    #pragma unroll
+                        for (int q = 0; q < Q; ++q) s[q] = 1.0f / (1.0f + __expf(-x[q]));
+                    } else {
+                        float sum = 0.0f;
+    #pragma unroll
+                        for (int q = 0; q < Q; ++q) {
+                            s[q] = __expf(x[q] - m);
+                            sum += s[q];
+                        }
+                        largest = 1.0f / wave_allreduce_sum(sum);
+    #pragma unroll
+                        for (int q = 0; q < Q; ++q) s[q] *= largest;
+                    }
+                    // two choices' errors, with the sum's with the bias
+                    margin = 2.0f * 0x1p-24f * (1.0f + (Q + 34.0f) * largest + 2.0f * top_b);
+                }
+    #pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    if constexpr (BIAS) s[q] += b[q];
+                    const float c = BIAS ? s[q] : x[q];
+                    const bool out = !(x[q] > kNegInf) || (BIAS && !(c > kNegInf));
+                    key[q] = out ? 0u : key_of(c);
+                    if constexpr (GROUPS) s[q] = out ? kNegInf : s[q];
+                    few_masks<Q>();
+                }
+                near = false;
+                if constexpr (GROUPS) {
+                    const int per = a.experts / a.groups;
+                    float *choice = (float *)choice_lds[wave];
+    #pragma unroll
+                    for (int q = 0; q < Q; ++q) choice[q * 64 + lane] = s[q];
+                    wave_lds_sync();
+                    const float score = lane < a.groups ? group_score(choice + lane * per, per, a.group_top) : kNegInf;
+                    wave_lds_sync();
+                    const unsigned long long kept =
+                        best_groups(score, a.groups, a.top_groups, 2.5f * margin, near);
+    #pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int g = (q * 64 + lane) / per;  // of an absent expert, whose key is 0: any
+                        key[q] = (kept >> (g & 63)) & 1 ? key[q] : 0u;
+                        few_masks<Q>();
+                    }
+                }
+                // k places, and one more for how far the last of them is from what stays out
+                float before = __builtin_huge_valf();
+                const int places = a.k + (BIAS ? 1 : 0);
+                for (int i = 0; i < places && !near; ++i) {
+                    uint32_t v = key[0];
+    #pragma unroll
+                    for (int q = 1; q < Q; ++q) v = max(v, key[q]);
+                    v = wave_max_u32(v);
+                    if (v == 0) break;
+                    if constexpr (BIAS) {
+                        const float c = of_key(v);
+                        near = i > 0 && before - c <= margin;
+                        before = c;
+                    }
+                    int at = 0;
+    #pragma unroll
+                    for (int q = Q - 1; q >= 0; --q) {
+                        const unsigned long long w = __ballot(key[q] == v);
+                        if (w != 0) at = q * 64 + __builtin_ctzll(w);
+                        few_masks<Q>();
+                    }
+                    if (i < a.k && lane == i) id = at;
+    #pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        if (at == q * 64 + lane) key[q] = 0;
+                        few_masks<Q>();
+                    }
                 }
             }
-        const double score = a.group_top == 2 && second > kLow ? best + second : best;
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const double o = __shfl(score, g, 64);
-            rank += o > score || (o == score && g < lane);
+            if constexpr (kExact)
+                if (near) id = exact_ids<T, Q, SIGMOID>(a, a.X, (size_t)row * a.ldx, m, choice_lds[wave], coef);
         }
-        const unsigned long long kept = __ballot(lane < a.groups && rank < a.top_groups);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int g = (q * 64 + lane) / per;
-            if (g >= a.groups || !((kept >> g) & 1)) c[q] = kLow;
+        // the weights, in binary64: place i in lane i
+        const float xi = id >= 0 ? logit_at<T>(a.X, (size_t)row * a.ldx, id, a.experts) : kNegInf;
+        double w = score64<SIGMOID>(xi, m, coef);
+        if (renorm) {
+            const double total = wave_sum64(w);
+            w = total > 0.0 ? w / total : 0.0;
+        } else if constexpr (!SIGMOID) {
+            double sum = 0.0;
+#pragma unroll 1
+            for (int e0 = 0; e0 < a.experts; e0 += 64)
+                sum += score64<false>(logit_at<T>(a.X, (size_t)row * a.ldx, e0 + lane, a.experts), m, coef);
+            sum = wave_sum64(sum);
+            w = sum > 0.0 ? w / sum : 0.0;
         }
-    }
-    int my_id = -1;
-    double my_s = 0.0, total = 0.0;
-    for (int i = 0; i < a.k; ++i) {
-        double v = kLow, sv = 0.0;
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (c[q] > v) {
-                v = c[q];
-                sv = s[q];
-                at = q * 64 + lane;
-            }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double vo = shfl_xor64(v, d), so = shfl_xor64(sv, d);
-            const int ao = __shfl_xor(at, d, 64);
-            if (vo > v || (vo == v && ao < at)) {
-                v = vo;
-                sv = so;
-                at = ao;
-            }
-        }
-        if (at == 0x7fffffff || bad) break;   // no expert left (the same in every lane)
-        if (lane == i) {
-            my_id = at;
-            my_s = sv;
-        }
-        total += sv;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (at == q * 64 + lane) c[q] = kLow;
-    }
-    if (live && lane < a.k) {
-        double w = my_s;
-        if (renorm) w = total > 0.0 ? w / total : 0.0;
         w *= (double)a.scale;
-        if (my_id < 0) w = bad ? __builtin_nan("") : 0.0;
-        a.ids[(size_t)row * a.k + lane] = my_id;
-        a.weights[(size_t)row * a.k + lane] = (float)w;
-        if (a.counts != nullptr && my_id >= 0) atomicAdd(a.counts + my_id, 1);
+        if (id < 0) w = bad ? __builtin_nan("") : 0.0;
+        if (lane < a.k) {
+            a.ids[(size_t)row * a.k + lane] = id;
+            a.weights[(size_t)row * a.k + lane] = (float)w;
+            if (count && id >= 0) atomicAdd(&hist[id], 1);
+        }
+    }
+    if (!count) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += 64 * kRouteWaves) {
+        const int n = hist[e];
+        if (single) a.counts[e] = n;
+        else if (n > 0) atomicAdd(a.counts + e, n);
     }
 }
 
@@ -298,21 +534,30 @@ gemm355_status gemm355_route(int dtype, unsigned flags, int rows, int experts, i
     }
     if (rows == 0 && counts == nullptr) return GEMM355_OK;
     if (!current_device_is_gfx950()) return GEMM355_ERR_DEVICE;
-    if (counts != nullptr) {
+    const bool single = rows > 0 && rows <= kRouteWaves;  // one workgroup writes the counts itself
+    if (counts != nullptr && !single) {
         hipLaunchKernelGGL(zero_counts_kernel, dim3(cdiv(experts, 256)), dim3(256), 0, stream, experts, counts);
         if (hipGetLastError() != hipSuccess) return GEMM355_ERR_LAUNCH;
     }
     if (rows == 0) return GEMM355_OK;
     const RouteArgs a{rows, experts, k, groups, top_groups, group_top, X, ldx, bias, scale, ids, weights, counts};
     const bool renorm = flags & GEMM355_ROUTE_RENORM;
+    const dim3 grid(cdiv(rows, kRouteWaves) < kRouteGrid ? cdiv(rows, kRouteWaves) : kRouteGrid), block(64 * kRouteWaves);
     const hipError_t e = by_type_and_width(dtype, experts, [&](auto t, auto q) {
         using T = decltype(t);
         constexpr int Q = decltype(q)::value;
-        const dim3 grid(cdiv(rows, 4));
+        const auto go = [&](auto sig, auto has_bias, auto in_groups) {
+            hipLaunchKernelGGL((route_kernel<T, Q, decltype(sig)::value, decltype(has_bias)::value,
+                                             decltype(in_groups)::value>),
+                               grid, block, 0, stream, a, renorm, single);
+        };
+        const auto with = [&](auto sig, auto has_bias) {
+            top_groups < groups ? go(sig, has_bias, std::true_type{}) : go(sig, has_bias, std::false_type{});
+        };
         if (flags & GEMM355_ROUTE_SIGMOID)
-            hipLaunchKernelGGL((route_kernel<T, Q, true>), grid, dim3(256), 0, stream, a, renorm);
+            bias != nullptr ? with(std::true_type{}, std::true_type{}) : with(std::true_type{}, std::false_type{});
         else
-            hipLaunchKernelGGL((route_kernel<T, Q, false>), grid, dim3(256), 0, stream, a, renorm);
+            bias != nullptr ? with(std::false_type{}, std::true_type{}) : with(std::false_type{}, std::false_type{});
         return hipGetLastError();
     });
     return e == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH;

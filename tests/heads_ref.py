@@ -147,7 +147,8 @@ def route(X, dtype, k, kind="softmax", bias=None, groups=1, top_groups=1, group_
             for g in keep:
                 mask[g * per:(g + 1) * per] = False
             c = np.where(mask, -np.inf, c)
-        order = [e for e in sorted(range(E), key=lambda e: (-c[e], e)) if c[e] > -np.inf][:k]
+        by = c if bias is not None else np.where(c > -np.inf, x[r], -np.inf)
+        order = [e for e in sorted(range(E), key=lambda e: (-by[e], e)) if c[e] > -np.inf][:k]
         ids[r, :len(order)] = order
         w = s[r][order]
         if renorm:

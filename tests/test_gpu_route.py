@@ -126,6 +126,31 @@ def test_route_masked_experts(kind):
             check_route(X, "f32", 8, kind=kind, renorm=renorm, **kw)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 200, 512, 1000])
+def test_route_choices_a_rounding_apart(kind, E):
+    """Choices and group scores that binary32 cannot order, and some it can: steps of 2^-30 and
+    2^-22 of the scores, hidden in logits that the bias evens out."""
+    rng = np.random.default_rng(E)
+    X = ref.make_router(40, E, "f32", E)
+    s = ref.scores(X.astype(np.float64), kind)
+    # rows 0..: every choice near 0.5, its distance from it the rounding of the bias
+    bias = (0.5 - s[0]).astype(np.float32)
+    X[1:20] = X[0]
+    X[1:20] += (rng.integers(-1, 2, (19, E)) * np.spacing(np.abs(X[0]))).astype(np.float32)
+    check_route(X, "f32", 8, kind=kind, bias=bias, renorm=True)
+    check_route(X, "f32", 8, kind=kind, bias=bias, groups=4, top_groups=2, group_top=2)
+    # group scores equal but for the last bits: the same logits in every group, reordered
+    per = E // 4
+    for r in range(20, 40):
+        base = X[r, :per].copy()
+        for g in range(4):
+            X[r, g * per:(g + 1) * per] = rng.permutation(base)
+        X[r, rng.integers(E)] += np.float32(1e-6)
+    check_route(X, "f32", 8, kind=kind, groups=4, top_groups=2, group_top=2, renorm=True)
+    check_route(X, "f32", 8, kind=kind, groups=4, top_groups=1, group_top=1)
+
+
 def test_route_chosen_scores_of_zero():
     # the bias chooses experts whose softmax is 0 in binary64 (800 below the maximum)
     X = np.full((2, 32), -800.0, np.float32)

@@ -168,6 +168,9 @@ gemm355_status gemm355_route(int dtype, unsigned flags, int rows, int experts, i
  *     ds_e = sum_{i: ids_i = e} q_i
  *     softmax: dX_e = s_e (ds_e - sum_f ds_f s_f);   sigmoid: dX_e = ds_e s_e (1 - s_e)
  *
+ * With RENORM, and with sigmoid scores, only the chosen logits of a row enter its gradient,
+ * and no other is read.
+ *
  * dX (rows x experts, type `dtype`, row stride lddx) may equal X when lddx == ldx; any
  * other overlap is an argument error.  Arguments as for gemm355_route. */
 gemm355_status gemm355_route_grad(int dtype, unsigned flags, int rows, int experts, int k,

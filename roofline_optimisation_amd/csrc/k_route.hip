@@ -38,6 +38,20 @@ struct RouteArgs {
     int32_t *counts;
 };
 
+// The arguments (the kernel's first) as they lie in memory, behind a pointer the compiler
+// cannot see through: what is rarely needed is loaded where it is used instead of being held
+// in scalar registers from the kernel's start.
+#ifdef __HIP_DEVICE_COMPILE__
+typedef const __attribute__((address_space(4))) RouteArgs *ArgsPtr;
+#else
+typedef const RouteArgs *ArgsPtr;  // the host pass only parses the kernels
+#endif
+__device__ __forceinline__ ArgsPtr args_in_memory() {
+    ArgsPtr p = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 template <typename T>
 __device__ __forceinline__ float load_elem(const void *p, size_t i) {
     return to_float(((const T *)p)[i]);
@@ -89,35 +103,73 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 
 __device__ __forceinline__ float wave_max(float v) { return of_key(wave_max_u32(key_of(v))); }
 
-// Which of the groups' scores (one per lane) are among the `top` largest, ties to the lowest
-// group; `near`: two scores lie within `margin` of each other.
+// The two largest of a lane's values and of those the other lane of an exchange holds.
 template <typename F>
-__device__ __forceinline__ unsigned long long best_groups(F score, int groups, int top, F margin, bool &near) {
-    const int lane = threadIdx.x % 64;
+__device__ __forceinline__ void merge_two(F &best, F &second, F bo, F so) {
+    second = fmax(fmax(second, so), fmin(best, bo));
+    best = fmax(best, bo);
+}
+
+// A group's score, in every one of its lanes: group g of `per` experts (choices in LDS) is
+// scanned by the S = 64 / (groups rounded up to a power of two) lanes from g S on.
+__device__ __forceinline__ float group_score32(const float *choice, int per, int S, int sub, int group_top) {
+    constexpr float kNegInf = -__builtin_huge_valf();
+    float best = kNegInf, second = kNegInf;
+#pragma unroll 1
+    for (int i = sub; i < per; i += S) {
+        const float v = choice[i];
+        second = fmaxf(second, fminf(best, v));
+        best = fmaxf(best, v);
+    }
+    if (S > 1) merge_two(best, second, DppXchg<kDppQuadXor1>::get(best), DppXchg<kDppQuadXor1>::get(second));
+    if (S > 2) merge_two(best, second, DppXchg<kDppQuadXor2>::get(best), DppXchg<kDppQuadXor2>::get(second));
+    if (S > 4)
+        merge_two(best, second, DppXchg<kDppRowHalfMirror>::get(best), DppXchg<kDppRowHalfMirror>::get(second));
+    if (S > 8) merge_two(best, second, DppXchg<kDppRowMirror>::get(best), DppXchg<kDppRowMirror>::get(second));
+    if (S > 16) merge_two(best, second, SwapHalves16::get(best), SwapHalves16::get(second));
+    return group_top == 2 && second > kNegInf ? best + second : best;
+}
+
+// Which of the groups are among the `top` of the largest score, ties to the lowest group;
+// near: two scores lie within `margin` of each other.  A lane holds the score of group
+// lane / S.
+__device__ __forceinline__ unsigned long long best_groups32(float score, int groups, int top, int shift,
+                                                            float margin, bool &near) {
+    const int mine = (int)(threadIdx.x % 64) >> shift;
+    const uint32_t key = key_of(score);
     int rank = 0;
     bool close = false;
 #pragma unroll 1
     for (int g = 0; g < groups; ++g) {
-        const F o = __shfl(score, g, 64);
-        rank += o > score || (o == score && g < lane);
-        close |= g != lane && o - score <= margin && score - o <= margin;
+        const float o = read_lane(score, g << shift);
+        rank += key_of(o) >= key + (g < mine ? 0u : 1u);
+        close |= g != mine && fabsf(o - score) <= margin;
     }
-    near = __any(close && lane < groups);
+    near = __any(close && mine < groups);
+    const unsigned long long in = __ballot(rank < top);   // S lanes a group
+    unsigned long long kept = 0;
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) kept |= ((in >> (g << shift)) & 1) << g;
+    return kept;
+}
+
+// The same on binary64 scores, lane g holding group g's.
+__device__ __forceinline__ unsigned long long best_groups64(double score, int groups, int top) {
+    const int lane = threadIdx.x % 64;
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+        const double o = __shfl(score, g, 64);
+        rank += o > score || (o == score && g < lane);
+    }
     return __ballot(lane < groups && rank < top);
 }
 
-// A group's score from the choices of its experts (in the wave's LDS row, `per` of them).
-template <typename F>
-__device__ __forceinline__ F group_score(const F *choice, int per, int group_top) {
-    const F low = (F)kLow;
-    F best = low, second = low;
-#pragma unroll 4
-    for (int i = 0; i < per; ++i) {
-        const F v = choice[i];
-        second = fmax(second, fmin(best, v));
-        best = fmax(best, v);
-    }
-    return group_top == 2 && second > low ? best + second : best;
+__device__ __forceinline__ double group_score64(const double *choice, int per, int group_top) {
+    double best = kLow, second = kLow;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) merge_two(best, second, choice[i], kLow);
+    return group_top == 2 && second > kLow ? best + second : best;
 }
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -169,8 +221,10 @@ __device__ __forceinline__ float logit_at(const void *X, size_t x0, int e, int e
 // the wave's row of LDS, of which a lane touches its own experts only, but for the groups'
 // scores.  Rows that come here are few, so this keeps to few registers.
 template <typename T, int Q, bool SIGMOID>
-__device__ __forceinline__ int exact_ids(const RouteArgs &a, const void *X, size_t x0, float m, double *choice,
-                                         const double *coef) {
+__device__ __forceinline__ int exact_ids(size_t row, float m, double *choice, const double *coef) {
+    const RouteArgs a = *args_in_memory();
+    const void *X = a.X;
+    const size_t x0 = row * a.ldx;
     const int lane = threadIdx.x % 64;
     double sum = 0.0;
 #pragma unroll 1
@@ -192,11 +246,10 @@ __device__ __forceinline__ int exact_ids(const RouteArgs &a, const void *X, size
     const int per = a.experts / a.groups;
     if (a.top_groups < a.groups) {
         wave_lds_sync();
-        const double own = group_score(choice + min(lane, a.groups - 1) * per, per, a.group_top);
+        const double own = group_score64(choice + min(lane, a.groups - 1) * per, per, a.group_top);
         const double score = lane < a.groups ? own : kLow;
         wave_lds_sync();
-        bool near;
-        kept = best_groups(score, a.groups, a.top_groups, 0.0, near);
+        kept = best_groups64(score, a.groups, a.top_groups);
     }
 #pragma unroll 1
     for (int e0 = 0; e0 < a.experts; e0 += 64) {
@@ -233,19 +286,12 @@ __device__ __forceinline__ int exact_ids(const RouteArgs &a, const void *X, size
     return id;
 }
 
-// With 8 experts per lane or more, keeps one expert's lane masks (two scalar registers each) from
-// being formed before the last one's are used.
-template <int Q>
-__device__ __forceinline__ void few_masks() {
-    if constexpr (Q >= 8) __builtin_amdgcn_sched_barrier(0);
-}
-
 // Rows of more than 512 experts are always decided on binary64 scores: 16 keys and their lane
 // masks per lane do not fit the scalar registers.
 constexpr bool has_keys(int Q) { return Q <= 8; }
 
-constexpr int kRouteWaves = 8;
-constexpr int kRouteGrid = 1024;  // workgroups; each takes every kRouteGrid-th group of rows
+constexpr int kRouteWaves = 16;
+constexpr int kRouteGrid = 512;  // workgroups; each takes every kRouteGrid-th group of rows
 
 // BIAS: choices add a.bias.  GROUPS: a.top_groups < a.groups.  SINGLE: one workgroup takes
 // every row, and writes the counts; else they are added to.
@@ -302,7 +348,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
                     float largest = 1.0f;
                     if constexpr (SIGMOID) {
     #pragma unroll
-                        for (int q = 0; q < Q; ++q) s[q] = 1.0f / (1.0f + __expf(-x[q]));
+                        for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[q]));
                     } else {
                         float sum = 0.0f;
     #pragma unroll
@@ -324,24 +370,27 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
                     const bool out = !(x[q] > kNegInf) || (BIAS && !(c > kNegInf));
                     key[q] = out ? 0u : key_of(c);
                     if constexpr (GROUPS) s[q] = out ? kNegInf : s[q];
-                    few_masks<Q>();
                 }
                 near = false;
                 if constexpr (GROUPS) {
-                    const int per = a.experts / a.groups;
+                    const ArgsPtr am = args_in_memory();
+                    const int groups = am->groups, per = a.experts / groups;
                     float *choice = (float *)choice_lds[wave];
     #pragma unroll
                     for (int q = 0; q < Q; ++q) choice[q * 64 + lane] = s[q];
                     wave_lds_sync();
-                    const float score = lane < a.groups ? group_score(choice + lane * per, per, a.group_top) : kNegInf;
+                    // S lanes a group, S = 2^shift
+                    const int shift = __builtin_clz((unsigned)groups - 1) - 26;  // two groups or more
+                    const int mine = min(lane >> shift, groups - 1);
+                    const float score = group_score32(choice + mine * per, per, 1 << shift,
+                                                      lane & ((1 << shift) - 1), am->group_top);
                     wave_lds_sync();
                     const unsigned long long kept =
-                        best_groups(score, a.groups, a.top_groups, 2.5f * margin, near);
-    #pragma unroll
+                        best_groups32(score, groups, am->top_groups, shift, 2.5f * margin, near);
+#pragma unroll
                     for (int q = 0; q < Q; ++q) {
                         const int g = (q * 64 + lane) / per;  // of an absent expert, whose key is 0: any
                         key[q] = (kept >> (g & 63)) & 1 ? key[q] : 0u;
-                        few_masks<Q>();
                     }
                 }
                 // k places, and one more for how far the last of them is from what stays out
@@ -362,19 +411,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
     #pragma unroll
                     for (int q = Q - 1; q >= 0; --q) {
                         const unsigned long long w = __ballot(key[q] == v);
-                        if (w != 0) at = q * 64 + __builtin_ctzll(w);
-                        few_masks<Q>();
+                        at = w != 0 ? q * 64 + __builtin_ctzll(w) : at;
                     }
                     if (i < a.k && lane == i) id = at;
     #pragma unroll
                     for (int q = 0; q < Q; ++q) {
-                        if (at == q * 64 + lane) key[q] = 0;
-                        few_masks<Q>();
+                        if (at >> 6 == q) key[q] = lane == (at & 63) ? 0u : key[q];   // one q: a scalar branch
                     }
                 }
             }
             if constexpr (kExact)
-                if (near) id = exact_ids<T, Q, SIGMOID>(a, a.X, (size_t)row * a.ldx, m, choice_lds[wave], coef);
+                if (near) id = exact_ids<T, Q, SIGMOID>(row, m, choice_lds[wave], coef);
         }
         // the weights, in binary64: place i in lane i
         const float xi = id >= 0 ? logit_at<T>(a.X, (size_t)row * a.ldx, id, a.experts) : kNegInf;
@@ -390,114 +437,195 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
             sum = wave_sum64(sum);
             w = sum > 0.0 ? w / sum : 0.0;
         }
-        w *= (double)a.scale;
+        const ArgsPtr am = args_in_memory();
+        w *= (double)am->scale;
         if (id < 0) w = bad ? __builtin_nan("") : 0.0;
         if (lane < a.k) {
-            a.ids[(size_t)row * a.k + lane] = id;
-            a.weights[(size_t)row * a.k + lane] = (float)w;
+            am->ids[(size_t)row * a.k + lane] = id;
+            am->weights[(size_t)row * a.k + lane] = (float)w;
             if (count && id >= 0) atomicAdd(&hist[id], 1);
         }
     }
     if (!count) return;
     __syncthreads();
+    int32_t *counts = args_in_memory()->counts;
     for (int e = threadIdx.x; e < a.experts; e += 64 * kRouteWaves) {
         const int n = hist[e];
-        if (single) a.counts[e] = n;
-        else if (n > 0) atomicAdd(a.counts + e, n);
+        if (single) counts[e] = n;
+        else if (n > 0) atomicAdd(counts + e, n);
     }
 }
 
-// The gradient: one wave per row, Q experts per lane.
-template <typename T, int Q, bool SIGMOID>
-__global__ __launch_bounds__(256) void route_grad_kernel(int rows, int experts, int k, const void *X,
-                                                         int ldx, const int32_t *ids,
-                                                         const float *dweights, float scale, void *dX,
-                                                         int lddx, bool renorm) {
+// Sums and maxima over aligned runs of n lanes, n a power of two; in every lane.
+template <typename Op>
+__device__ __forceinline__ float over_lanes(float v, int n, Op op) {
+    if (n > 1) v = op(v, DppXchg<kDppQuadXor1>::get(v));
+    if (n > 2) v = op(v, DppXchg<kDppQuadXor2>::get(v));
+    if (n > 4) v = op(v, DppXchg<kDppRowHalfMirror>::get(v));
+    if (n > 8) v = op(v, DppXchg<kDppRowMirror>::get(v));
+    if (n > 16) v = op(v, SwapHalves16::get(v));
+    if (n > 32) v = op(v, __shfl_xor(v, 32, 64));
+    return v;
+}
+__device__ __forceinline__ float lanes_sum(float v, int n) {
+    return over_lanes(v, n, [](float x, float y) { return x + y; });
+}
+__device__ __forceinline__ float lanes_max(float v, int n) {
+    return over_lanes(v, n, [](float x, float y) { return fmaxf(x, y); });
+}
+
+// Adds each lane's v at its place (an index into the wave's row of LDS, -1 for none), places
+// that several lanes of a row share in the order of their slots.  The row holds zeros.
+__device__ __forceinline__ void scatter_add(float *row, int place, float v, int slot, int k) {
+    const int lane = threadIdx.x % 64;
+    int *tag = (int *)row;
+    if (place >= 0) tag[place] = lane;
+    wave_lds_sync();
+    const bool shared = place >= 0 && tag[place] != lane;
+    wave_lds_sync();
+    if (!__any(shared)) {
+        if (place >= 0) row[place] = v;
+    } else {
+        if (place >= 0) row[place] = 0.0f;
+        wave_lds_sync();
+        for (int j = 0; j < k; ++j) {
+            if (slot == j && place >= 0) row[place] += v;
+            wave_lds_sync();
+        }
+    }
+    wave_lds_sync();
+}
+
+constexpr int kGradLds = 2048;  // floats of LDS per wave: the rows it takes at once
+
+// The gradient where only chosen experts have one: sigmoid scores, and renormalised softmax
+// (sum_f ds_f s_f is 0 there, and q_i s_i = w_i (dw_i - sum_j w_j dw_j) with w the softmax of
+// the chosen logits alone).  Only k logits of a row are read.  A wave takes R rows, n lanes a
+// row (n a power of two, at least k), a chosen expert per lane; the rows are put together in
+// LDS and written whole.  Bound by the bytes written: with a row per wave and every
+// expert compared with every place the arithmetic took 18.8 us for 16384 rows of 256.
+template <typename T, bool SIGMOID, bool VEC>
+__global__ __launch_bounds__(256) void route_grad_chosen_kernel(int rows, int experts, int k, const void *X, int ldx,
+                                                                const int32_t *ids, const float *dweights,
+                                                                float scale, void *dX, int lddx, bool renorm,
+                                                                int n, int R) {
+    __shared__ __attribute__((aligned(16))) float lds[4][kGradLds];
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int row0 = (blockIdx.x * 4 + wave) * R;
+    if (row0 >= rows) return;  // a whole wave; no barrier in this kernel
+    float *out = lds[wave];
+    const int live = min(R, rows - row0);
+    for (int c = 4 * lane; c < live * experts; c += 256) *(floatx4 *)(out + c) = floatx4{0.f, 0.f, 0.f, 0.f};
+    const int r = lane / n, slot = lane & (n - 1);
+    int id = -1;
+    float g = 0.0f;
+    if (r < live && slot < k) {
+        id = ids[(size_t)(row0 + r) * k + slot];
+        g = scale * dweights[(size_t)(row0 + r) * k + slot];
+    }
+    const bool on = id >= 0 && id < experts;
+    const float x = on ? load_elem<T>(X, (size_t)(row0 + r) * ldx + id) : -__builtin_huge_valf();
+    g = on ? g : 0.0f;
+    float v;
+    if constexpr (SIGMOID) {
+        const float s = on ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        if (renorm) {
+            const float sum = lanes_sum(s, n), inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            g = (g - lanes_sum(g * s, n) * inv) * inv;
+        }
+        v = g * s * (1.0f - s);
+    } else {
+        const float m = lanes_max(x, n);
+        const float e = x > -__builtin_huge_valf() ? expf(x - m) : x != x ? x : 0.0f;
+        const float sum = lanes_sum(e, n), w = sum == 0.0f ? 0.0f : e / sum;
+        v = w * (g - lanes_sum(g * w, n));
+    }
+    wave_lds_sync();
+    scatter_add(out, on ? r * experts + id : -1, v, slot, k);
+    for (int i = 0; i < live; ++i) {
+        const float *o = out + i * experts;
+        const size_t at = (size_t)(row0 + i) * lddx;
+        if constexpr (VEC) {
+            for (int c = 4 * lane; c < experts; c += 256) {
+                const floatx4 f = *(const floatx4 *)(o + c);
+                if constexpr (std::is_same<T, float>::value) {
+                    *(floatx4 *)((float *)dX + at + c) = f;
+                } else {
+                    const uint2 h = make_uint2((uint32_t)to_bits(f[0], T{}) | (uint32_t)to_bits(f[1], T{}) << 16,
+                                               (uint32_t)to_bits(f[2], T{}) | (uint32_t)to_bits(f[3], T{}) << 16);
+                    *(uint2 *)((uint16_t *)dX + at + c) = h;
+                }
+            }
+        } else {
+            for (int c = lane; c < experts; c += 64) store_elem<T>(dX, at + c, o[c]);
+        }
+    }
+}
+
+// The gradient of plain softmax weights, where every expert has one: one wave per row, Q
+// experts per lane.
+template <typename T, int Q>
+__global__ __launch_bounds__(256) void route_grad_kernel(int rows, int experts, int k, const void *X, int ldx,
+                                                         const int32_t *ids, const float *dweights, float scale,
+                                                         void *dX, int lddx) {
+    __shared__ __attribute__((aligned(16))) float lds[4][Q * 64];
     const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int row = blockIdx.x * 4 + wave;
-    if (row >= rows) return;
-    float s[Q], ds[Q];
-    float m = -__builtin_huge_valf();
+    if (row >= rows) return;  // a whole wave; no barrier in this kernel
+    float *sum_of = lds[wave];
+    float s[Q], m = -__builtin_huge_valf();
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        const int e = q * 64 + lane;
-        s[q] = e < experts ? load_elem<T>(X, (size_t)row * ldx + e) : -__builtin_huge_valf();
-        ds[q] = 0.0f;
+        s[q] = logit_at<T>(X, (size_t)row * ldx, q * 64 + lane, experts);
+        sum_of[q * 64 + lane] = 0.0f;
         m = fmaxf(m, s[q]);
     }
-    if constexpr (SIGMOID) {
+    const int id = lane < k ? ids[(size_t)row * k + lane] : -1;
+    const float g = lane < k ? scale * dweights[(size_t)row * k + lane] : 0.0f;
+    wave_lds_sync();
+    scatter_add(sum_of, id >= 0 && id < experts ? id : -1, g, lane, k);
+    m = lanes_max(m, 64);
+    const float shift = m == -__builtin_huge_valf() ? 0.0f : m;
+    float sum = 0.0f;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) s[q] = 1.0f / (1.0f + expf(-s[q]));
-    } else {
-        for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
-        const float shift = m == -__builtin_huge_valf() ? 0.0f : m;
-        float sum = 0.0f;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            s[q] = expf(s[q] - shift);
-            sum += s[q];
-        }
-        sum = wave_allreduce_sum(sum);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a NaN row stays NaN
-#pragma unroll
-        for (int q = 0; q < Q; ++q) s[q] *= inv;
+    for (int q = 0; q < Q; ++q) {
+        s[q] = expf(s[q] - shift);
+        sum += s[q];
     }
-    const int32_t *id = ids + (size_t)row * k;
-    const float *dw = dweights + (size_t)row * k;
-    float sum_s = 0.0f, sum_qs = 0.0f;   // this lane's share over its chosen experts
-    for (int i = 0; i < k; ++i) {
-        const int e = id[i];
-        const float g = scale * dw[i];
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (e == q * 64 + lane && e < experts) {
-                ds[q] += g;
-                sum_s += s[q];
-                sum_qs += g * s[q];
-            }
-    }
-    if (renorm) {
-        sum_s = wave_allreduce_sum(sum_s);
-        sum_qs = wave_allreduce_sum(sum_qs);
-        const float inv = sum_s == 0.0f ? 0.0f : 1.0f / sum_s;
-        const float mean = sum_qs * inv;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) ds[q] = 0.0f;
-        for (int i = 0; i < k; ++i) {
-            const int e = id[i];
-            const float g = (scale * dw[i] - mean) * inv;
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-                if (e == q * 64 + lane && e < experts) ds[q] += g;
-        }
-    }
+    sum = wave_allreduce_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a NaN row stays NaN
     float dot = 0.0f;
-    if constexpr (!SIGMOID) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) dot += ds[q] * s[q];
-        dot = wave_allreduce_sum(dot);
+    for (int q = 0; q < Q; ++q) {
+        s[q] *= inv;
+        dot += sum_of[q * 64 + lane] * s[q];
     }
+    dot = wave_allreduce_sum(dot);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int e = q * 64 + lane;
-        const float d = SIGMOID ? ds[q] * s[q] * (1.0f - s[q]) : s[q] * (ds[q] - dot);
-        if (e < experts) store_elem<T>(dX, (size_t)row * lddx + e, d);
+        if (e < experts) store_elem<T>(dX, (size_t)row * lddx + e, s[q] * (sum_of[e] - dot));
     }
+}
+
+// f(T{}) for the storage type.
+template <typename F>
+hipError_t by_type(int dtype, F f) {
+    if (dtype == kF32) return f(0.0f);
+    if (dtype == kF16) return f(f16_t{});
+    return f(bf16_t{});
 }
 
 // f(T{}, integral_constant<int, Q>) for the storage type and the experts per lane.
 template <typename F>
 hipError_t by_type_and_width(int dtype, int experts, F f) {
-    const auto width = [&](auto t) -> hipError_t {
+    return by_type(dtype, [&](auto t) -> hipError_t {
         if (experts <= 64) return f(t, std::integral_constant<int, 1>{});
         if (experts <= 128) return f(t, std::integral_constant<int, 2>{});
         if (experts <= 256) return f(t, std::integral_constant<int, 4>{});
         if (experts <= 512) return f(t, std::integral_constant<int, 8>{});
         return f(t, std::integral_constant<int, 16>{});
-    };
-    if (dtype == kF32) return width(0.0f);
-    if (dtype == kF16) return width(f16_t{});
-    return width(bf16_t{});
+    });
 }
 
 }  // namespace
@@ -583,19 +711,32 @@ gemm355_status gemm355_route_grad(int dtype, unsigned flags, int rows, int exper
     if (d.meets(Span(ids, (size_t)rows * k * 4)) || d.meets(Span(dweights, (size_t)rows * k * 4)))
         return GEMM355_ERR_INVALID_ARG;
     if (!current_device_is_gfx950()) return GEMM355_ERR_DEVICE;
-    const bool renorm = flags & GEMM355_ROUTE_RENORM;
-    const hipError_t e = by_type_and_width(dtype, experts, [&](auto t, auto q) {
-        using T = decltype(t);
-        constexpr int Q = decltype(q)::value;
-        const dim3 grid(cdiv(rows, 4));
-        if (flags & GEMM355_ROUTE_SIGMOID)
-            hipLaunchKernelGGL((route_grad_kernel<T, Q, true>), grid, dim3(256), 0, stream, rows, experts, k, X,
-                               ldx, ids, dweights, scale, dX, lddx, renorm);
-        else
-            hipLaunchKernelGGL((route_grad_kernel<T, Q, false>), grid, dim3(256), 0, stream, rows, experts, k, X,
-                               ldx, ids, dweights, scale, dX, lddx, renorm);
-        return hipGetLastError();
-    });
+    const bool renorm = flags & GEMM355_ROUTE_RENORM, sigmoid = flags & GEMM355_ROUTE_SIGMOID;
+    hipError_t e;
+    if (sigmoid || renorm) {
+        int n = 1;
+        while (n < k) n *= 2;
+        const int fit = kGradLds / experts, R = fit < 64 / n ? fit : 64 / n;
+        const bool vec = experts % 4 == 0 && lddx % 4 == 0 && (uintptr_t)dX % (4 * es) == 0;
+        const dim3 grid(cdiv(rows, 4 * R));
+        e = by_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            const auto go = [&](auto sig, auto v) {
+                hipLaunchKernelGGL((route_grad_chosen_kernel<T, decltype(sig)::value, decltype(v)::value>), grid,
+                                   dim3(256), 0, stream, rows, experts, k, X, ldx, ids, dweights, scale, dX, lddx,
+                                   renorm, n, R);
+            };
+            if (sigmoid) vec ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+            else vec ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+            return hipGetLastError();
+        });
+    } else {
+        e = by_type_and_width(dtype, experts, [&](auto t, auto q) {
+            hipLaunchKernelGGL((route_grad_kernel<decltype(t), decltype(q)::value>), dim3(cdiv(rows, 4)), dim3(256), 0,
+                               stream, rows, experts, k, X, ldx, ids, dweights, scale, dX, lddx);
+            return hipGetLastError();
+        });
+    }
     return e == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH;
 }
 

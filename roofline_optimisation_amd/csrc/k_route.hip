@@ -65,11 +65,25 @@ __device__ __forceinline__ void store_elem(void *p, size_t i, float v) {
 // The same value in every lane: the other lane's copy of a binary64 value at xor distance d.
 __device__ __forceinline__ double shfl_xor64(double v, int d) { return __shfl_xor(v, d, 64); }
 
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += shfl_xor64(v, d);
+template <class X>
+__device__ __forceinline__ double exchange64(double v) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    const float lo = X::get(__builtin_bit_cast(float, (uint32_t)u)), hi = X::get(__builtin_bit_cast(float, (uint32_t)(u >> 32)));
+    return __builtin_bit_cast(double, (unsigned long long)__builtin_bit_cast(uint32_t, lo) |
+                                          (unsigned long long)__builtin_bit_cast(uint32_t, hi) << 32);
+}
+
+// The sum over the first n lanes of an aligned run (n a power of two), in every one of them.
+__device__ __forceinline__ double lanes_sum64(double v, int n) {
+    if (n > 1) v += exchange64<DppXchg<kDppQuadXor1>>(v);
+    if (n > 2) v += exchange64<DppXchg<kDppQuadXor2>>(v);
+    if (n > 4) v += exchange64<DppXchg<kDppRowHalfMirror>>(v);
+    if (n > 8) v += exchange64<DppXchg<kDppRowMirror>>(v);
+    if (n > 16) v += exchange64<SwapHalves16>(v);
+    if (n > 32) v += shfl_xor64(v, 32);
     return v;
 }
+__device__ __forceinline__ double wave_sum64(double v) { return lanes_sum64(v, 64); }
 
 __global__ void zero_counts_kernel(int n, int32_t *counts) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
@@ -98,7 +112,11 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     v = max(v, dpp_u32<kDppRowMirror>(v));
     const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
     const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-    return max(max(a, b), max(c, d));
+    uint32_t e, f;   // on the scalar unit (left to itself the compiler takes these to the vector one)
+    asm("s_max_u32 %0, %1, %2" : "=s"(e) : "s"(a), "s"(b) : "scc");
+    asm("s_max_u32 %0, %1, %2" : "=s"(f) : "s"(c), "s"(d) : "scc");
+    asm("s_max_u32 %0, %0, %1" : "+s"(e) : "s"(f) : "scc");
+    return e;
 }
 
 __device__ __forceinline__ float wave_max(float v) { return of_key(wave_max_u32(key_of(v))); }
@@ -110,66 +128,59 @@ __device__ __forceinline__ void merge_two(F &best, F &second, F bo, F so) {
     best = fmax(best, bo);
 }
 
+template <class X>
+__device__ __forceinline__ float exchange(float v) { return X::get(v); }
+template <class X>
+__device__ __forceinline__ double exchange(double v) { return exchange64<X>(v); }
+
 // A group's score, in every one of its lanes: group g of `per` experts (choices in LDS) is
 // scanned by the S = 64 / (groups rounded up to a power of two) lanes from g S on.
-__device__ __forceinline__ float group_score32(const float *choice, int per, int S, int sub, int group_top) {
-    constexpr float kNegInf = -__builtin_huge_valf();
-    float best = kNegInf, second = kNegInf;
+template <typename F>
+__device__ __forceinline__ F group_score(const F *choice, int per, int S, int sub, int group_top) {
+    constexpr F low = (F)kLow;
+    F best = low, second = low;
 #pragma unroll 1
-    for (int i = sub; i < per; i += S) {
-        const float v = choice[i];
-        second = fmaxf(second, fminf(best, v));
-        best = fmaxf(best, v);
-    }
-    if (S > 1) merge_two(best, second, DppXchg<kDppQuadXor1>::get(best), DppXchg<kDppQuadXor1>::get(second));
-    if (S > 2) merge_two(best, second, DppXchg<kDppQuadXor2>::get(best), DppXchg<kDppQuadXor2>::get(second));
+    for (int i = sub; i < per; i += S) merge_two(best, second, choice[i], low);
+    if (S > 1) merge_two(best, second, exchange<DppXchg<kDppQuadXor1>>(best), exchange<DppXchg<kDppQuadXor1>>(second));
+    if (S > 2) merge_two(best, second, exchange<DppXchg<kDppQuadXor2>>(best), exchange<DppXchg<kDppQuadXor2>>(second));
     if (S > 4)
-        merge_two(best, second, DppXchg<kDppRowHalfMirror>::get(best), DppXchg<kDppRowHalfMirror>::get(second));
-    if (S > 8) merge_two(best, second, DppXchg<kDppRowMirror>::get(best), DppXchg<kDppRowMirror>::get(second));
-    if (S > 16) merge_two(best, second, SwapHalves16::get(best), SwapHalves16::get(second));
-    return group_top == 2 && second > kNegInf ? best + second : best;
+        merge_two(best, second, exchange<DppXchg<kDppRowHalfMirror>>(best), exchange<DppXchg<kDppRowHalfMirror>>(second));
+    if (S > 8) merge_two(best, second, exchange<DppXchg<kDppRowMirror>>(best), exchange<DppXchg<kDppRowMirror>>(second));
+    if (S > 16) merge_two(best, second, exchange<SwapHalves16>(best), exchange<SwapHalves16>(second));
+    return group_top == 2 && second > low ? best + second : best;
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) { return read_lane(v, lane); }
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    return __builtin_bit_cast(double, (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)u, lane) |
+                                          (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane)
+                                              << 32);
 }
 
 // Which of the groups are among the `top` of the largest score, ties to the lowest group;
-// near: two scores lie within `margin` of each other.  A lane holds the score of group
-// lane / S.
-__device__ __forceinline__ unsigned long long best_groups32(float score, int groups, int top, int shift,
-                                                            float margin, bool &near) {
+// near: a kept score lies within `margin` of one that is not.  A lane holds the score of
+// group lane >> shift.
+template <typename F>
+__device__ __forceinline__ unsigned long long best_groups(F score, int groups, int top, int shift, F margin,
+                                                          bool &near) {
     const int mine = (int)(threadIdx.x % 64) >> shift;
-    const uint32_t key = key_of(score);
     int rank = 0;
-    bool close = false;
+    int close = 0;   // groups ahead of mine by no more than the margin
 #pragma unroll 1
     for (int g = 0; g < groups; ++g) {
-        const float o = read_lane(score, g << shift);
-        rank += key_of(o) >= key + (g < mine ? 0u : 1u);
-        close |= g != mine && fabsf(o - score) <= margin;
+        const F o = lane_value(score, g << shift);
+        const bool ahead = o > score || (o == score && g < mine);
+        rank += ahead;
+        close += ahead && o - score <= margin;
     }
-    near = __any(close && mine < groups);
-    const unsigned long long in = __ballot(rank < top);   // S lanes a group
+    // not kept, and one that is (ranks below top) among those just ahead
+    near = __any(mine < groups && rank >= top && rank - close < top);
+    const unsigned long long in = __ballot(rank < top);   // 2^shift lanes a group
     unsigned long long kept = 0;
 #pragma unroll 1
     for (int g = 0; g < groups; ++g) kept |= ((in >> (g << shift)) & 1) << g;
     return kept;
-}
-
-// The same on binary64 scores, lane g holding group g's.
-__device__ __forceinline__ unsigned long long best_groups64(double score, int groups, int top) {
-    const int lane = threadIdx.x % 64;
-    int rank = 0;
-#pragma unroll 1
-    for (int g = 0; g < groups; ++g) {
-        const double o = __shfl(score, g, 64);
-        rank += o > score || (o == score && g < lane);
-    }
-    return __ballot(lane < groups && rank < top);
-}
-
-__device__ __forceinline__ double group_score64(const double *choice, int per, int group_top) {
-    double best = kLow, second = kLow;
-#pragma unroll 1
-    for (int i = 0; i < per; ++i) merge_two(best, second, choice[i], kLow);
-    return group_top == 2 && second > kLow ? best + second : best;
 }
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -217,55 +228,95 @@ __device__ __forceinline__ float logit_at(const void *X, size_t x0, int e, int e
     return e < experts ? x : -__builtin_huge_valf();
 }
 
-// The row's ids by binary64 scores: id of place i in lane i.  x: the row's logits, choice:
-// the wave's row of LDS, of which a lane touches its own experts only, but for the groups'
-// scores.  Rows that come here are few, so this keeps to few registers.
-template <typename T, int Q, bool SIGMOID>
-__device__ __forceinline__ int exact_ids(size_t row, float m, double *choice, const double *coef) {
-    const RouteArgs a = *args_in_memory();
-    const void *X = a.X;
-    const size_t x0 = row * a.ldx;
-    const int lane = threadIdx.x % 64;
+// What the scores of a row are divided by: softmax's sum, or 1.
+template <typename T, bool SIGMOID>
+__device__ __forceinline__ double divisor64(const void *X, size_t x0, int experts, float m, const double *coef) {
+    if constexpr (SIGMOID) return 1.0;
     double sum = 0.0;
 #pragma unroll 1
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const double v = score64<SIGMOID>(logit_at<T>(X, x0, e0 + lane, a.experts), m, coef);
-        choice[e0 + lane] = v;
-        sum += v;
-    }
-    sum = SIGMOID ? 1.0 : wave_sum64(sum);
+    for (int e0 = 0; e0 < experts; e0 += 64)
+        sum += score64<false>(logit_at<T>(X, x0, e0 + (int)(threadIdx.x % 64), experts), m, coef);
+    return wave_sum64(sum);
+}
+
+// An expert's choice in binary64, -infinity for a masked or absent one and for a NaN bias.
+template <typename T, bool SIGMOID>
+__device__ __forceinline__ double choice64(const void *X, size_t x0, const float *bias, int e, int experts, float m,
+                                           double sum, const double *coef) {
+    const float x = logit_at<T>(X, x0, e, experts);
+    const double c = score64<SIGMOID>(x, m, coef) / sum + (bias != nullptr ? (double)bias[min(e, experts - 1)] : 0.0);
+    return x > -__builtin_huge_valf() && c > kLow ? c : kLow;
+}
+
+// The lanes a group's score is found by: 2^shift of them.
+__device__ __forceinline__ int group_shift(int groups) {
+    return groups > 1 ? __builtin_clz((unsigned)groups - 1) - 26 : 6;
+}
+
+// The row's kept groups by binary64 choices, which are left in the wave's row of LDS.
+template <typename T, int Q, bool SIGMOID>
+__device__ __forceinline__ unsigned long long exact_groups(size_t row, float m, double *choice, const double *coef) {
+    const ArgsPtr a = args_in_memory();
+    const int lane = threadIdx.x % 64, experts = a->experts, groups = a->groups;
+    const void *X = a->X;
+    const float *bias = a->bias;
+    const size_t x0 = row * a->ldx;
+    const double sum = divisor64<T, SIGMOID>(X, x0, experts, m, coef);
 #pragma unroll 1
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int e = e0 + lane;
-        const float b = a.bias != nullptr ? a.bias[min(e, a.experts - 1)] : 0.0f;
-        const double c = choice[e] / sum + (double)b;
-        const bool in = logit_at<T>(X, x0, e, a.experts) > -__builtin_huge_valf() && c > kLow;
-        choice[e] = in ? c : kLow;   // masked, absent, NaN bias
-    }
-    unsigned long long kept = ~0ull;
-    const int per = a.experts / a.groups;
-    if (a.top_groups < a.groups) {
-        wave_lds_sync();
-        const double own = group_score64(choice + min(lane, a.groups - 1) * per, per, a.group_top);
-        const double score = lane < a.groups ? own : kLow;
-        wave_lds_sync();
-        kept = best_groups64(score, a.groups, a.top_groups);
-    }
+    for (int e0 = 0; e0 < Q * 64; e0 += 64)
+        choice[e0 + lane] = choice64<T, SIGMOID>(X, x0, bias, e0 + lane, experts, m, sum, coef);
+    if (a->top_groups >= groups) return ~0ull;
+    wave_lds_sync();
+    const int shift = group_shift(groups), mine = min(lane >> shift, groups - 1), per = experts / groups;
+    const double score = group_score(choice + mine * per, per, 1 << shift, lane & ((1 << shift) - 1), a->group_top);
+    wave_lds_sync();
+    bool near;
+    return best_groups(score, groups, a->top_groups, shift, 0.0, near);
+}
+
+// The ids of the row's first places put in the order of their binary64 choices.
+template <typename T, bool SIGMOID>
+__device__ __forceinline__ int exact_order(size_t row, float m, int id, const double *coef) {
+    const ArgsPtr a = args_in_memory();
+    const int lane = threadIdx.x % 64;
+    const size_t x0 = row * a->ldx;
+    const double sum = divisor64<T, SIGMOID>(a->X, x0, a->experts, m, coef);
+    const bool in = id >= 0;   // of the first lanes
+    const double c = in ? choice64<T, SIGMOID>(a->X, x0, a->bias, max(id, 0), a->experts, m, sum, coef) : kLow;
+    const int n = __builtin_popcountll(__ballot(in));
+    int rank = 0;
 #pragma unroll 1
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    for (int i = 0; i < n; ++i) {
+        const double o = lane_value(c, i);
+        const int oid = __builtin_amdgcn_readlane(id, i);
+        rank += o > c || (o == c && oid < id);
+    }
+    return __builtin_amdgcn_ds_permute(4 * (in ? rank : lane), id);
+}
+
+// The row's ids wholly by binary64 choices: id of place i in lane i.  choice: the wave's row
+// of LDS, of which a lane touches its own experts only, but for the groups' scores.
+template <typename T, int Q, bool SIGMOID>
+__device__ __forceinline__ int exact_ids(size_t row, float m, double *choice, const double *coef) {
+    const unsigned long long kept = exact_groups<T, Q, SIGMOID>(row, m, choice, coef);
+    const ArgsPtr a = args_in_memory();
+    const int lane = threadIdx.x % 64, experts = a->experts, per = experts / a->groups, k = a->k;
+    const bool by_logit = a->bias == nullptr;
+#pragma unroll 1
+    for (int e0 = 0; e0 < experts; e0 += 64) {
         const int e = e0 + lane;
         double c = choice[e];
         // without a bias the order within the kept groups is the logits'
-        if (a.bias == nullptr && c > kLow) c = (double)logit_at<T>(X, x0, e, a.experts);
+        if (by_logit && c > kLow) c = (double)logit_at<T>(a->X, row * a->ldx, e, experts);
         choice[e] = (kept >> ((e / per) & 63)) & 1 ? c : kLow;
     }
     int id = -1;
 #pragma unroll 1
-    for (int i = 0; i < a.k; ++i) {
+    for (int i = 0; i < k; ++i) {
         double v = kLow;
         int at = 0x7fffffff;
 #pragma unroll 1
-        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        for (int e0 = 0; e0 < experts; e0 += 64) {
             const double c = choice[e0 + lane];
             at = c > v ? e0 + lane : at;
             v = fmax(c, v);
@@ -319,6 +370,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
         }
         top_b = wave_max(top_b);
     }
+    int per = 1, group_of[Q];   // of an absent expert, whose key is 0: any group
+    if constexpr (GROUPS && has_keys(Q)) {
+        per = a.experts / a.groups;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) group_of[q] = ((q * 64 + lane0) / per) & 63;
+    }
     for (int row = blockIdx.x * kRouteWaves + wave; row < a.rows; row += gridDim.x * kRouteWaves) {
         // the lane as each row's own value, or the masks of absent experts, two scalar registers
         // each, are kept across rows
@@ -329,13 +386,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             x[q] = logit_at<T>(a.X, (size_t)row * a.ldx, q * 64 + lane, a.experts);
-            bad |= x[q] != x[q] || (!SIGMOID && x[q] == __builtin_huge_valf());
+            // NaN, and for softmax +infinity
+            bad |= __builtin_amdgcn_classf(x[q], SIGMOID ? 0x003 : 0x203);
             m = fmaxf(m, x[q]);
         }
         bad = __any(bad);
-        m = wave_max(m);
+        if constexpr (!SIGMOID) m = wave_max(m);
         int id = -1;
-        if (!bad && m > kNegInf) {
+        if (!bad && (SIGMOID || m > kNegInf)) {
             bool near = true;
             if constexpr (has_keys(Q)) {
                 // binary32 scores s, each within 2^-24 (1 + (E / 64 + 32) s) of the exact one: a
@@ -347,23 +405,23 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
                 if constexpr (BIAS || GROUPS) {
                     float largest = 1.0f;
                     if constexpr (SIGMOID) {
-    #pragma unroll
+#pragma unroll
                         for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[q]));
                     } else {
                         float sum = 0.0f;
-    #pragma unroll
+#pragma unroll
                         for (int q = 0; q < Q; ++q) {
                             s[q] = __expf(x[q] - m);
                             sum += s[q];
                         }
                         largest = 1.0f / wave_allreduce_sum(sum);
-    #pragma unroll
+#pragma unroll
                         for (int q = 0; q < Q; ++q) s[q] *= largest;
                     }
                     // two choices' errors, with the sum's with the bias
                     margin = 2.0f * 0x1p-24f * (1.0f + (Q + 34.0f) * largest + 2.0f * top_b);
                 }
-    #pragma unroll
+#pragma unroll
                 for (int q = 0; q < Q; ++q) {
                     if constexpr (BIAS) s[q] += b[q];
                     const float c = BIAS ? s[q] : x[q];
@@ -374,50 +432,65 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
                 near = false;
                 if constexpr (GROUPS) {
                     const ArgsPtr am = args_in_memory();
-                    const int groups = am->groups, per = a.experts / groups;
+                    const int groups = am->groups;
                     float *choice = (float *)choice_lds[wave];
-    #pragma unroll
+#pragma unroll
                     for (int q = 0; q < Q; ++q) choice[q * 64 + lane] = s[q];
                     wave_lds_sync();
-                    // S lanes a group, S = 2^shift
-                    const int shift = __builtin_clz((unsigned)groups - 1) - 26;  // two groups or more
+                    const int shift = group_shift(groups);
                     const int mine = min(lane >> shift, groups - 1);
-                    const float score = group_score32(choice + mine * per, per, 1 << shift,
-                                                      lane & ((1 << shift) - 1), am->group_top);
+                    const float score = group_score((const float *)choice + mine * per, per, 1 << shift,
+                                                    lane & ((1 << shift) - 1), am->group_top);
                     wave_lds_sync();
-                    const unsigned long long kept =
-                        best_groups32(score, groups, am->top_groups, shift, 2.5f * margin, near);
+                    bool close;
+                    unsigned long long kept = best_groups(score, groups, am->top_groups, shift, 2.5f * margin, close);
+                    if (close) kept = exact_groups<T, Q, SIGMOID>(row, m, choice_lds[wave], coef);
 #pragma unroll
-                    for (int q = 0; q < Q; ++q) {
-                        const int g = (q * 64 + lane) / per;  // of an absent expert, whose key is 0: any
-                        key[q] = (kept >> (g & 63)) & 1 ? key[q] : 0u;
-                    }
+                    for (int q = 0; q < Q; ++q) key[q] = (kept >> group_of[q]) & 1 ? key[q] : 0u;
                 }
-                // k places, and one more for how far the last of them is from what stays out
-                float before = __builtin_huge_valf();
-                const int places = a.k + (BIAS ? 1 : 0);
-                for (int i = 0; i < places && !near; ++i) {
-                    uint32_t v = key[0];
-    #pragma unroll
+                // The places, the i-th key in lane i as its id.  With a bias, one more to see
+                // how far the last is from what stays out: neighbours closer than the margin
+                // are put in order in binary64, and if the one after the last is as close to
+                // the next, the row is left to binary64 choices altogether.
+                uint32_t my_key = 0, v = 0;
+                const auto next = [&]() {
+                    v = key[0];
+#pragma unroll
                     for (int q = 1; q < Q; ++q) v = max(v, key[q]);
                     v = wave_max_u32(v);
+                };
+                const int places = BIAS ? min(a.k + 1, 64) : a.k;
+                for (int i = 0; i < places; ++i) {
+                    next();
                     if (v == 0) break;
-                    if constexpr (BIAS) {
-                        const float c = of_key(v);
-                        near = i > 0 && before - c <= margin;
-                        before = c;
-                    }
                     int at = 0;
-    #pragma unroll
+#pragma unroll
                     for (int q = Q - 1; q >= 0; --q) {
                         const unsigned long long w = __ballot(key[q] == v);
                         at = w != 0 ? q * 64 + __builtin_ctzll(w) : at;
                     }
-                    if (i < a.k && lane == i) id = at;
-    #pragma unroll
-                    for (int q = 0; q < Q; ++q) {
+                    const bool here = lane == i;
+                    id = here ? at : id;
+                    if constexpr (BIAS) my_key = here ? v : my_key;
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
                         if (at >> 6 == q) key[q] = lane == (at & 63) ? 0u : key[q];   // one q: a scalar branch
+                }
+                if constexpr (BIAS) {
+                    const uint32_t after = __shfl_down(my_key, 1, 64);
+                    const bool close = lane < 63 && after != 0 && of_key(my_key) - of_key(after) <= margin;
+                    const unsigned long long w = __ballot(close);   // lane i: places i and i + 1
+                    if (w != 0) {
+                        bool lost = places == 64;   // no lane for the one after the last
+                        if (!lost && ((w >> (places - 2)) & 1)) {
+                            const uint32_t last = __builtin_amdgcn_readlane(my_key, places - 1);
+                            next();
+                            lost = v != 0 && of_key(last) - of_key(v) <= margin;
+                        }
+                        near = lost;
+                        if (!lost) id = exact_order<T, SIGMOID>(row, m, id, coef);
                     }
+                    id = lane < a.k ? id : -1;
                 }
             }
             if constexpr (kExact)
@@ -427,7 +500,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bo
         const float xi = id >= 0 ? logit_at<T>(a.X, (size_t)row * a.ldx, id, a.experts) : kNegInf;
         double w = score64<SIGMOID>(xi, m, coef);
         if (renorm) {
-            const double total = wave_sum64(w);
+            const double total = lanes_sum64(w, a.k <= 8 ? 8 : 64);
             w = total > 0.0 ? w / total : 0.0;
         } else if constexpr (!SIGMOID) {
             double sum = 0.0;

@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int N, in
                                                         const int64_t *__restrict__ labels, int64_t ignore,
                                                         const float *__restrict__ lse,
                                                         const float *__restrict__ dloss, int rescale,
-                                                        float *scale, RowGrad *rows, E *Xm, int ldm) {
+                                                        float *scale, RowGrad *rows, E *Xm, int ldm, int vec) {
     __shared__ float sm[4];
     float S = 1.0f;
     if (rescale) {
@@ -174,10 +174,19 @@ __global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int N, in
         const int64_t y = r < M ? labels[r] : -1;
         const bool live = r < M && y != ignore && y >= 0 && y < N;
         if (threadIdx.x == 0)
-            rows[r] = live ? RowGrad{lse[r], dloss[r] * S, (int)y, 0} : RowGrad{0.0f, 0.0f, -1, 0};
+            rows[r] = RowGrad{live ? lse[r] : 0.0f, live ? dloss[r] * S : 0.0f, live ? (int)y : -1, 0};
         const E *x = X + (size_t)r * ldx;
         E *o = Xm + (size_t)r * ldm;
-        for (int c = threadIdx.x; c < ldm; c += 256) o[c] = live && c < K ? x[c] : E{};
+        if (vec) {   // rows of X and Xm 16-byte aligned, K a whole number of 16-byte chunks
+            constexpr int kV = 16 / sizeof(E);
+            for (int c = kV * threadIdx.x; c < ldm; c += kV * 256) {
+                u32x4 v = {0, 0, 0, 0};
+                if (live && c < K) v = *(const u32x4 *)(x + c);
+                *(u32x4 *)(o + c) = v;
+            }
+        } else {
+            for (int c = threadIdx.x; c < ldm; c += 256) o[c] = live && c < K ? x[c] : E{};
+        }
     }
 }
 
@@ -200,21 +209,36 @@ __global__ __launch_bounds__(256) void xent_dz_kernel(int nc, int v0, const floa
 }
 
 // out = scale[1] * (the sum of `splits` partial sums, `stride` apart), rounded to the 16-bit
-// type.  Grid: (columns / 1024, rows).
-template <typename T>
+// type; four columns per thread (VEC: in one access each).  Grid: (columns / 1024, rows).
+template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *__restrict__ acc, int lda,
                                                          int splits, size_t stride,
                                                          const float *__restrict__ scale, uint16_t *out,
                                                          int ldo) {
+    const int c = blockIdx.x * 1024 + 4 * (int)threadIdx.x;
+    if (c >= cols) return;
     const float f = scale[1];
+    const float *a = acc + (size_t)blockIdx.y * lda + c;
+    uint16_t *o = out + (size_t)blockIdx.y * ldo + c;
+    if constexpr (VEC) {
+        floatx4 v = *(const floatx4 *)a;
+        int i = 1;
+        for (; i + 4 <= splits; i += 4) {   // four loads in flight, added in order
+            floatx4 w[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int c = blockIdx.x * 1024 + 256 * u + (int)threadIdx.x;
-        if (c >= cols) break;
-        const float *a = acc + (size_t)blockIdx.y * lda + c;
-        float v = a[0];
-        for (int i = 1; i < splits; ++i) v += a[i * stride];
-        out[(size_t)blockIdx.y * ldo + c] = to_bits(f * v, T{});
+            for (int u = 0; u < 4; ++u) w[u] = *(const floatx4 *)(a + (i + u) * stride);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v += w[u];
+        }
+        for (; i < splits; ++i) v += *(const floatx4 *)(a + i * stride);
+        *(uint2 *)o = make_uint2((uint32_t)to_bits(f * v[0], T{}) | (uint32_t)to_bits(f * v[1], T{}) << 16,
+                                 (uint32_t)to_bits(f * v[2], T{}) | (uint32_t)to_bits(f * v[3], T{}) << 16);
+    } else {
+        for (int u = 0; u < 4 && c + u < cols; ++u) {
+            float v = a[u];
+            for (int i = 1; i < splits; ++i) v += a[i * stride + u];
+            o[u] = to_bits(f * v, T{});
+        }
     }
 }
 
@@ -483,13 +507,15 @@ struct GradCall {
 
 hipError_t prep(const GradCall &a, int Mp, float *scale, RowGrad *rows, void *Xm, int ldm) {
     const dim3 grid(Mp < 1024 ? Mp : 1024);
+    const size_t es = a.dtype == kF32 ? 4 : 2;
+    const int vec = rows_aligned16(a.X, a.ldx, (int)es) && a.K % (16 / es) == 0;
     if (a.dtype == kF32)
         hipLaunchKernelGGL((xent_prep_kernel<float>), grid, dim3(256), 0, a.s, a.M, Mp, a.N, a.K, (const float *)a.X,
-                           a.ldx, a.labels, a.ignore, a.lse, a.dloss, 0, scale, rows, (float *)Xm, ldm);
+                           a.ldx, a.labels, a.ignore, a.lse, a.dloss, 0, scale, rows, (float *)Xm, ldm, vec);
     else
         hipLaunchKernelGGL((xent_prep_kernel<uint16_t>), grid, dim3(256), 0, a.s, a.M, Mp, a.N, a.K,
                            (const uint16_t *)a.X, a.ldx, a.labels, a.ignore, a.lse, a.dloss,
-                           a.dtype == kF16 ? 1 : 0, scale, rows, (uint16_t *)Xm, ldm);
+                           a.dtype == kF16 ? 1 : 0, scale, rows, (uint16_t *)Xm, ldm, vec);
     return hipGetLastError();
 }
 
@@ -511,14 +537,16 @@ hipError_t piece_dz(const GradCall &a, const GradPlan &p, int v0, int nc) {
 
 hipError_t round16(const GradCall &a, int rows, int cols, const float *acc, int lda, int splits, size_t stride,
                    const float *scale, void *out, int ldo) {
+    const bool vec = cols % 4 == 0 && lda % 4 == 0 && stride % 4 == 0 && ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
     return over_rows(rows, [&](int r, int n) {
-        const dim3 grid(cdiv(cols, 1024), n);
-        if (a.dtype == kF16)
-            hipLaunchKernelGGL((xent_round_kernel<f16_t>), grid, dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda,
-                               splits, stride, scale, (uint16_t *)out + (size_t)r * ldo, ldo);
-        else
-            hipLaunchKernelGGL((xent_round_kernel<bf16_t>), grid, dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda,
-                               splits, stride, scale, (uint16_t *)out + (size_t)r * ldo, ldo);
+        const auto go = [&](auto t, auto v) {
+            hipLaunchKernelGGL((xent_round_kernel<decltype(t), decltype(v)::value>), dim3(cdiv(cols, 1024), n),
+                               dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda, splits, stride, scale,
+                               (uint16_t *)out + (size_t)r * ldo, ldo);
+        };
+        const auto typed = [&](auto t) { vec ? go(t, std::true_type{}) : go(t, std::false_type{}); };
+        if (a.dtype == kF16) typed(f16_t{});
+        else typed(bf16_t{});
     });
 }
 

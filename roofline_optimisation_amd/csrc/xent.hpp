@@ -10,7 +10,7 @@ namespace g355 {
 
 // What the gradient needs of a row: its log-sum-exp, the upstream gradient (scaled) and the
 // label, -1 for a row without one (whose lse and g are 0 and whose copy of X is 0).
-struct RowGrad { float lse, g; int label, unused; };
+struct alignas(16) RowGrad { float lse, g; int label, unused; };
 
 // Z = X.op(W) of M rows and N classes; with trans_b W holds a class per row.  Rows start on
 // 16-byte boundaries, K is a multiple of 8 and at least 128, and a K x N W has N a multiple

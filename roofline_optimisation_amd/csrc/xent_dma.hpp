@@ -55,6 +55,16 @@ struct StatsEpilogue {
         const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4;
         float2 *const out = part + (size_t)(col0 / (16 * kNB)) * ldp;
         constexpr float kNegInf = -__builtin_huge_valf();
+        // the four labels of a lane's next quad row are loaded while this one's are used
+        int64_t next[4];
+        const auto load_labels = [&](int i) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = row0 + 16 * i + 4 * q4 + r;
+                next[r] = labels[!EDGE || row < M ? row : 0];
+            }
+        };
+        load_labels(0);
 #pragma unroll
         for (int g = 0; g < kMB; g += 4) {
             constexpr int kI = kMB < 4 ? kMB : 4;
@@ -62,23 +72,27 @@ struct StatsEpilogue {
 #pragma unroll
             for (int ii = 0; ii < kI; ++ii) {
                 const int i = g + ii, r0 = row0 + 16 * i + 4 * q4;
+                int rel[4];   // the label's column within the tile, -1 outside
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = r0 + r;
+                    const int64_t d = next[r] - col0;
+                    rel[r] = d >= 0 && d < 16 * kNB && (!EDGE || (r0 + r < M && next[r] < N)) ? (int)d : -1;
+                }
+                if (i + 1 < kMB) load_labels(i + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
                     float x[kNB];
 #pragma unroll
                     for (int j = 0; j < kNB; ++j) {
                         x[j] = acc_read(acc[i][j][r]);
                         if (EDGE && col0 + 16 * j + c16 >= N) x[j] = kNegInf;
                     }
-                    // the label's logit, where its column is in this tile (of a row of many
-                    // columns few tiles hold any)
-                    const int64_t rel = (!EDGE || row < M) ? labels[row] - col0 : -1;
-                    const bool hit = rel >= 0 && rel < 16 * kNB;
-                    if (__any(hit)) {
+                    // the label's logit (of a row of many columns few tiles hold the label's)
+                    if (__any(rel[r] >= 0)) {
 #pragma unroll
                         for (int j = 0; j < kNB; ++j)
-                            if (hit && (int)rel == 16 * j + c16 && (!EDGE || col0 + (int)rel < N)) zl[row] = x[j];
+                            if (rel[r] == 16 * j + c16) zl[r0 + r] = x[j];
                     }
                     float m = x[0];
 #pragma unroll
@@ -126,13 +140,27 @@ struct DzEpilogue {
     __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
         const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4, odd = lane & 1;
         const int cw = col0 + (lane & 14) + 16 * odd, padded = (N + 7) & ~7;
-#pragma unroll
-        for (int i = 0; i < kMB; ++i)
+        // the data of a lane's next four rows are loaded while this quad row is computed
+        floatx4 next[4];
+        const auto load_rows = [&](int i) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = row0 + 16 * i + 4 * q4 + r;
-                RowGrad w{0.0f, 0.0f, -1, 0};
-                if (!EDGE || row < M) w = rg[row];
+                next[r] = *(const floatx4 *)(rg + (!EDGE || row < M ? row : 0));
+            }
+        };
+        load_rows(0);
+#pragma unroll
+        for (int i = 0; i < kMB; ++i) {
+            floatx4 now[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) now[r] = next[r];
+            if (i + 1 < kMB) load_rows(i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = row0 + 16 * i + 4 * q4 + r;
+                const RowGrad w = __builtin_bit_cast(RowGrad, now[r]);
                 const int hot = w.label - v0 - col0 - c16;
                 float d[kNB];
 #pragma unroll
@@ -148,6 +176,7 @@ struct DzEpilogue {
                     if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(o + 16 * j) = v;
                 }
             }
+        }
     }
 };
 

@@ -338,21 +338,85 @@ bool fused_weights(unsigned flags, int K, const void *W, int ldw) {
     return rows_aligned16(W, ldw, 2) && offsets_fit(flags & GEMM355_TRANS_B ? 256 : K, ldw);
 }
 
-// Rows of the tile (EM x 256) for M rows.
-int tile_rows(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+// The time of M x N logits in one kind of tile, in rounds of 256 x 256 tiles (one per CU):
+// rounds of resident tiles times what a round takes, measured at K = 2048 (bf16, us: 256 x
+// 256 46, 128 x 256 33, 64 x 256 29 with one per CU and 60 with two, 64 x 128 12, 64 x 64 8
+// and 14).  Few rows are bound by reading W, for which many small tiles do best: 16 x 32000 x
+// 2048 51 / 41 / 38 / 26 / 26 us in this order, 256 x 8000 x 2048 48 / 36 / 32 / 17 / 21,
+// 256 x 32000 x 2048 54 / 43 / 44 / 52 / 59, 512 x 32000 x 1024 37 / 45 / 47.
+double head_cost(int tile, int M, int N) {
+    constexpr double kOne[kHeadTiles] = {1.0, 0.72, 0.63, 0.27, 0.17}, kTwo[kHeadTiles] = {0, 0, 1.2, 0, 0.3};
+    const long tiles = (long)cdiv(M, kHeadRows[tile]) * cdiv(N, kHeadCols[tile]);
+    if (kTwo[tile] > 0 && tiles > 256) return (double)((tiles + 511) / 512) * kTwo[tile];
+    return (double)((tiles + 255) / 256) * kOne[tile];
+}
+
+int head_tile(int M, int N, int K) {
+    int best = kHead256;
+    for (int t = kHead128; t < kHeadTiles; ++t)
+        if (K >= kHeadTrip[t] && head_cost(t, M, N) < head_cost(best, M, N)) best = t;
+    return best;
+}
+
+// Columns [v0, v0 + cols) of a product in one kind of tile.
+struct Section { int v0, cols, tile; };
+
+// The columns of M x N logits in one section, or, where that leaves a last round of few
+// tiles, the whole rounds and the rest in the tiles that suit it (2047 x 50003 x 2048: 1568
+// tiles of 256 x 256 are 6 rounds and 32 tiles, 360 us; 6 rounds and 224 tiles of 64 x 128
+// 338).
+int head_sections(int M, int N, int K, Section out[2]) {
+    const int tile = head_tile(M, N, K);
+    out[0] = {0, N, tile};
+    const long down = cdiv(M, kHeadRows[tile]), rounds = down * cdiv(N, kHeadCols[tile]) / 256;
+    const int whole = (int)(rounds * 256 / down) * kHeadCols[tile];
+    if (tile > kHead128 || whole == 0 || whole >= N) return 1;
+    const int rest = head_tile(M, N - whole, K);
+    if (head_cost(tile, M, whole) + head_cost(rest, M, N - whole) > 0.97 * head_cost(tile, M, N)) return 1;
+    out[0].cols = whole;
+    out[1] = {whole, N - whole, rest};
+    return 2;
+}
+
+// dX's product: its 16-bit result is a sum over ranges of classes, whose partial sums grow
+// with the number of ranges that fill the CUs, so fewer rows take smaller tiles (M = 512, K
+// = 1024 in 16 ranges of 128 x 256 tiles against 32 of 256 x 256: 80 against 86 us with the
+// dZ before it; 1024 x 2048 the same, 2047 x 2048 479 against 436).
+int dx_tile(int M) { return M <= 64 ? kHead64 : M <= 512 ? kHead128 : kHead256; }
+
+// dW's product, `across` tiles of 256 over the hidden size: 128 x 128 tiles two per CU where
+// the sum over the rows is short and the stores of one tile hide behind the other's sum (512
+// x 32000 x 1024 81 against 85 us with the dZ before it, 16 x 32000 x 2048 75 against 85,
+// 1024 x 32000 x 2048 the same, 2047 457 against 489 the other way), and for the rest of a
+// longer one where whole rounds of 256 x 256 tiles leave less than half a round.
+int dw_sections(int M, int N, int K, Section out[2]) {
+    const long across = cdiv(K, 256), tiles = across * cdiv(N, 256);
+    out[0] = {0, N, M <= 1024 || tiles < 128 ? 128 : 256};
+    const int whole = (int)(tiles / 256 * 256 / across) * 256;
+    if (out[0].tile == 128 || whole == 0 || whole >= N || 2 * (tiles - across * (whole / 256)) > 256) return 1;
+    out[0].cols = whole;
+    out[1] = {whole, N - whole, 128};
+    return 2;
+}
 
 constexpr int kStatRows = 32768;  // rows whose block statistics are held at once
 
+int stat_blocks(const Section &c) {
+    return cdiv(c.cols, kHeadCols[c.tile]) * (kHeadCols[c.tile] / kStatCols[c.tile]);
+}
+
 struct FusedForwardPlan {
-    int rows, em, blocks, ldm;
+    int rows, blocks, ldm, sections;
+    Section section[2];
     float2 *part;
     float *zl;
     uint16_t *Xm;
     size_t bytes;
     FusedForwardPlan(int M, int N, int K, void *ws) {
         rows = M < kStatRows ? M : kStatRows;
-        em = tile_rows(rows);
-        blocks = cdiv(N, 256) * (256 / stat_cols(em));
+        sections = head_sections(rows, N, K, section);
+        blocks = 0;
+        for (int i = 0; i < sections; ++i) blocks += stat_blocks(section[i]);
         ldm = K;
         Carver c{(char *)ws};
         part = (float2 *)c.take((size_t)blocks * rows * sizeof(float2));
@@ -378,7 +442,7 @@ struct Splits {
 constexpr long kDzBytes = 1L << 29;  // dZ of a piece
 
 struct FusedGradPlan {
-    int cols, Mp, ldm, em, splits;
+    int cols, Mp, ldm, dx, splits;
     float *scale, *dX;
     RowGrad *rows;
     uint16_t *Xm, *dZ;
@@ -386,14 +450,14 @@ struct FusedGradPlan {
     FusedGradPlan(int M, int N, int K, void *ws) {
         Mp = (int)up((size_t)M, 128);  // whole ring trips of dW's product, zeros past M
         ldm = K;
-        em = tile_rows(M);
+        dx = dx_tile(M);
         const long fit = kDzBytes / 2 / Mp / 256 * 256;
         const int pieces = (int)((N + (fit < 256 ? 256 : fit) - 1) / (fit < 256 ? 256 : fit));
         cols = (int)up((size_t)cdiv(N, pieces), 256);
         while (cols < N && N % cols != 0 && N % cols < 256) cols += 256;
         // dX's product: as many ranges of a piece's classes as fill the 256 CUs
         const int nc = cols < N ? cols : N;
-        splits = Splits(nc, 256 / (cdiv(M, em) * cdiv(K, 256))).count;
+        splits = Splits(nc, 256 / (cdiv(M, kHeadRows[dx]) * cdiv(K, kHeadCols[dx]))).count;
         Carver c{(char *)ws};
         scale = (float *)c.take(8);
         rows = (RowGrad *)c.take((size_t)Mp * sizeof(RowGrad));
@@ -457,9 +521,15 @@ gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, con
             hipLaunchKernelGGL(xent_copy_kernel, dim3(rows), dim3(256), 0, s, K, (const uint16_t *)x, ldx, p.Xm, p.ldm);
             G355_TRY(hipGetLastError());
         }
-        const HeadArgs h{rows, N, K, copy ? p.Xm : x, copy ? p.ldm : ldx, W, ldw, (flags & GEMM355_TRANS_B) != 0};
-        G355_TRY(dtype == kF16 ? launch_xent_stats_f16(p.em, h, labels + r0, p.part, p.rows, p.zl, s)
-                               : launch_xent_stats_bf16(p.em, h, labels + r0, p.part, p.rows, p.zl, s));
+        float2 *part = p.part;
+        for (int i = 0; i < p.sections; ++i) {
+            const Section &c = p.section[i];
+            const HeadArgs h{rows, c.cols, K, copy ? p.Xm : x, copy ? p.ldm : ldx, at(W, w_offset(flags, c.v0, ldw), 2),
+                             ldw, (flags & GEMM355_TRANS_B) != 0};
+            G355_TRY(dtype == kF16 ? launch_xent_stats_f16(c.tile, h, labels + r0, c.v0, part, p.rows, p.zl, s)
+                                   : launch_xent_stats_bf16(c.tile, h, labels + r0, c.v0, part, p.rows, p.zl, s));
+            part += (size_t)stat_blocks(c) * p.rows;
+        }
         G355_TRY(merge(rows, N, p, labels + r0, ignore, loss ? loss + r0 : nullptr, lse ? lse + r0 : nullptr, s));
     }
     return GEMM355_OK;
@@ -558,9 +628,15 @@ gemm355_status gradient_fused(const GradCall &a, void *ws) {
     for (int v0 = 0; v0 < a.N; v0 += p.cols) {
         const int nc = a.N - v0 < p.cols ? a.N - v0 : p.cols;
         const auto *w = (const uint16_t *)at(a.W, w_offset(a.flags, v0, a.ldw), 2);
-        const HeadArgs h{p.Mp, nc, a.K, p.Xm, p.ldm, w, a.ldw, tb};
-        G355_TRY(f16 ? launch_xent_dz_f16(p.em, h, p.rows, v0, p.dZ, p.cols, a.s)
-                     : launch_xent_dz_bf16(p.em, h, p.rows, v0, p.dZ, p.cols, a.s));
+        Section part[2];
+        const int dz_parts = head_sections(p.Mp, nc, a.K, part);
+        for (int i = 0; i < dz_parts; ++i) {
+            const Section &c = part[i];
+            const HeadArgs h{p.Mp, c.cols, a.K, p.Xm, p.ldm, w + w_offset(a.flags, c.v0, a.ldw), a.ldw, tb};
+            uint16_t *dZ = p.dZ + c.v0;
+            G355_TRY(f16 ? launch_xent_dz_f16(c.tile, h, p.rows, v0 + c.v0, dZ, p.cols, a.s)
+                         : launch_xent_dz_bf16(c.tile, h, p.rows, v0 + c.v0, dZ, p.cols, a.s));
+        }
         if (a.dX != nullptr) {
             const Splits sp(nc, p.splits);
             ProductArgs q{};
@@ -583,25 +659,27 @@ gemm355_status gradient_fused(const GradCall &a, void *ws) {
                 q.ldo = a.K;
                 q.accumulate = v0 > 0;
             }
-            G355_TRY(f16 ? launch_xent_dx_f16(p.em, tb, q, a.s) : launch_xent_dx_bf16(p.em, tb, q, a.s));
+            G355_TRY(f16 ? launch_xent_dx_f16(p.dx, tb, q, a.s) : launch_xent_dx_bf16(p.dx, tb, q, a.s));
         }
-        if (a.dW != nullptr) {
+        const int dw_parts = a.dW != nullptr ? dw_sections(a.M, nc, a.K, part) : 0;
+        for (int i = 0; i < dw_parts; ++i) {
+            const Section &c = part[i];
+            const int padded = (int)up((size_t)c.cols, 8);
+            const uint16_t *dZ = p.dZ + c.v0;
             ProductArgs q{};
-            const int padded = (int)up((size_t)nc, 8);
             q.K = p.Mp;
-            q.A = tb ? p.dZ : p.Xm;
+            q.A = tb ? dZ : p.Xm;
             q.lda = tb ? p.cols : p.ldm;
-            q.B = tb ? p.Xm : p.dZ;
+            q.B = tb ? p.Xm : dZ;
             q.ldb = tb ? p.ldm : p.cols;
             q.M = tb ? padded : a.K;
             q.N = tb ? a.K : padded;
-            q.rows = tb ? nc : a.K;
-            q.cols = tb ? a.K : nc;
-            q.out = (uint16_t *)at(a.dW, w_offset(a.flags, v0, a.lddw), 2);
+            q.rows = tb ? c.cols : a.K;
+            q.cols = tb ? a.K : c.cols;
+            q.out = (uint16_t *)at(a.dW, w_offset(a.flags, v0 + c.v0, a.lddw), 2);
             q.ldo = a.lddw;
             q.factor = p.scale + 1;
-            const int tile = (long)cdiv(q.rows, 256) * cdiv(q.cols, 256) >= 256 ? 256 : 128;
-            G355_TRY(f16 ? launch_xent_dw_f16(tile, q, a.s) : launch_xent_dw_bf16(tile, q, a.s));
+            G355_TRY(f16 ? launch_xent_dw_f16(c.tile, q, a.s) : launch_xent_dw_bf16(c.tile, q, a.s));
         }
     }
     if (!one && a.dX != nullptr)

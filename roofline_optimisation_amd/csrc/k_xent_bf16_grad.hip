@@ -3,8 +3,8 @@
 
 namespace g355 {
 
-hipError_t launch_xent_dx_bf16(int em, bool b_mn, const ProductArgs &p, hipStream_t s) {
-    return launch_dx<bf16_t>(em, b_mn, p, s);
+hipError_t launch_xent_dx_bf16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s) {
+    return launch_dx<bf16_t>(tile, b_mn, p, s);
 }
 
 hipError_t launch_xent_dw_bf16(int tile, const ProductArgs &p, hipStream_t s) {

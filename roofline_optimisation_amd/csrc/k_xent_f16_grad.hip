@@ -3,8 +3,8 @@
 
 namespace g355 {
 
-hipError_t launch_xent_dx_f16(int em, bool b_mn, const ProductArgs &p, hipStream_t s) {
-    return launch_dx<f16_t>(em, b_mn, p, s);
+hipError_t launch_xent_dx_f16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s) {
+    return launch_dx<f16_t>(tile, b_mn, p, s);
 }
 
 hipError_t launch_xent_dw_f16(int tile, const ProductArgs &p, hipStream_t s) {

@@ -3,9 +3,9 @@
 
 namespace g355 {
 
-hipError_t launch_xent_stats_f16(int em, const HeadArgs &h, const int64_t *labels, float2 *part, int ldp,
-                                 float *zl, hipStream_t s) {
-    return launch_head<f16_t>(em, h, StatsEpilogue{h.M, h.N, labels, part, ldp, zl}, s);
+hipError_t launch_xent_stats_f16(int tile, const HeadArgs &h, const int64_t *labels, int v0, float2 *part,
+                                 int ldp, float *zl, hipStream_t s) {
+    return launch_head<f16_t>(tile, h, StatsEpilogue{h.M, h.N, v0, labels, part, ldp, zl}, s);
 }
 
 }  // namespace g355

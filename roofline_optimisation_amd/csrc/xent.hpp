@@ -24,20 +24,28 @@ struct HeadArgs {
     bool trans_b;
 };
 
-// Statistics of Z by blocks of stat_cols(em) columns: part[block * ldp + row] = (maximum,
-// sum of exp(z - maximum)) and, where a row's label falls into Z, zl[row] = its logit.
-// em: the tile's rows, 64, 128 or 256.
-constexpr int stat_cols(int em) { return em == 64 ? 64 : 128; }
-hipError_t launch_xent_stats_f16(int em, const HeadArgs &h, const int64_t *labels, float2 *part, int ldp,
-                                 float *zl, hipStream_t s);
-hipError_t launch_xent_stats_bf16(int em, const HeadArgs &h, const int64_t *labels, float2 *part, int ldp,
-                                  float *zl, hipStream_t s);
+// The tiles of a head's products, EM rows x EN columns.
+enum HeadTiles : int { kHead256 = 0, kHead128, kHead64, kHead64x128, kHead64x64, kHeadTiles };
+constexpr int kHeadRows[kHeadTiles] = {256, 128, 64, 64, 64};
+constexpr int kHeadCols[kHeadTiles] = {256, 256, 256, 128, 64};
+// A trip of the tile's ring of loads; K is at least one.
+constexpr int kHeadTrip[kHeadTiles] = {128, 128, 128, 256, 256};
+// Columns of one wave, a block of the row statistics.
+constexpr int kStatCols[kHeadTiles] = {128, 128, 64, 64, 32};
+
+// Statistics of Z, W pointing at class v0, by blocks of kStatCols[tile] columns: part[block *
+// ldp + row] = (maximum, sum of exp(z - maximum)) and, where a row's label is one of these
+// classes, zl[row] = its logit.
+hipError_t launch_xent_stats_f16(int tile, const HeadArgs &h, const int64_t *labels, int v0, float2 *part,
+                                 int ldp, float *zl, hipStream_t s);
+hipError_t launch_xent_stats_bf16(int tile, const HeadArgs &h, const int64_t *labels, int v0, float2 *part,
+                                  int ldp, float *zl, hipStream_t s);
 
 // dZ (M x N rounded up to a multiple of 8, row stride ldz, the added columns 0) of the
 // classes v0 .. v0 + N, W pointing at the first of them.
-hipError_t launch_xent_dz_f16(int em, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
+hipError_t launch_xent_dz_f16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
                               hipStream_t s);
-hipError_t launch_xent_dz_bf16(int em, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
+hipError_t launch_xent_dz_bf16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
                                hipStream_t s);
 
 // A product of the gradient: op(A).op(B) over K.  A is M x K (k-contiguous), or K x M with
@@ -62,9 +70,10 @@ struct ProductArgs {
 };
 
 // dX's product: A = dZ (k-contiguous), B m/n-contiguous or not; partial sums, or the 16-bit
-// result when p.part is NULL.  em x 256 tiles, em = 64, 128 or 256.
-hipError_t launch_xent_dx_f16(int em, bool b_mn, const ProductArgs &p, hipStream_t s);
-hipError_t launch_xent_dx_bf16(int em, bool b_mn, const ProductArgs &p, hipStream_t s);
+// result when p.part is NULL.  Tiles
+// kHead256, kHead128 and kHead64.
+hipError_t launch_xent_dx_f16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s);
+hipError_t launch_xent_dx_bf16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s);
 // dW's product: both operands m/n-contiguous, K a multiple of 128, 16-bit result.  Square
 // tiles of extent 128 or 256.
 hipError_t launch_xent_dw_f16(int tile, const ProductArgs &p, hipStream_t s);

@@ -42,7 +42,7 @@ __device__ __forceinline__ float acc_read(float v) {
 // lane's 4 quad rows, lane l%16 = c keeps the one of quad row c / 4, register c % 4, so that
 // 64 consecutive rows leave in one store.
 struct StatsEpilogue {
-    int M, N;
+    int M, N, v0;
     const int64_t *labels;
     float2 *part;
     int ldp;
@@ -75,8 +75,8 @@ struct StatsEpilogue {
                 int rel[4];   // the label's column within the tile, -1 outside
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int64_t d = next[r] - col0;
-                    rel[r] = d >= 0 && d < 16 * kNB && (!EDGE || (r0 + r < M && next[r] < N)) ? (int)d : -1;
+                    const int64_t d = next[r] - v0 - col0;
+                    rel[r] = d >= 0 && d < 16 * kNB && (!EDGE || (r0 + r < M && d < N - col0)) ? (int)d : -1;
                 }
                 if (i + 1 < kMB) load_labels(i + 1);
                 __builtin_amdgcn_sched_barrier(0);
@@ -218,49 +218,54 @@ struct RoundEpilogue {
     }
 };
 
-// EM x 256 tiles: 256 rows on 2 x 2 waves of 128 x 128, 128 rows on 2 x 2 of 64 x 128, 64
-// rows on 1 x 4 of 64 x 64; a 4-stage ring.
-template <int EM>
+// The tiles' waves and ring stages: 256 x 256 on 2 x 2 waves of 128 x 128, 128 x 256 on 2 x 2
+// of 64 x 128, 64 x 256 on 1 x 4 of 64 x 64, 64 x 128 and 64 x 64 on 2 x 2.
+template <int TILE>
 struct HeadTile {
-    static constexpr int kWM = EM == 64 ? 1 : 2, kWN = EM == 64 ? 4 : 2, kNs = 4;
-    using G = dma::Geo<EM, 256, kWM, kWN, kNs, 0>;
+    static constexpr int kEM = kHeadRows[TILE], kEN = kHeadCols[TILE];
+    static constexpr int kWM = TILE == kHead64 ? 1 : 2, kWN = 4 / kWM;
+    static constexpr int kNs = kHeadTrip[TILE] / dma::kBK;
+    static constexpr int kPerSimd = TILE == kHead64 || TILE == kHead64x64 ? 2 : 1;  // waves: workgroups per CU
+    using G = dma::Geo<kEM, kEN, kWM, kWN, kNs, 0>;
+    static_assert(kEN / kWN == kStatCols[TILE], "a statistics block is a wave's columns");
 };
 
-template <typename T, bool W_MN, int EM, bool KR, class EX>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EM == 64 ? 2 : 1)))
+template <typename T, bool W_MN, int TILE, bool KR, class EX>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(HeadTile<TILE>::kPerSimd)))
 void xent_head_kernel(int M, int N, int K, const uint16_t *__restrict__ X, int ldx,
                       const uint16_t *__restrict__ W, int ldw, EX ex) {
-    using H = HeadTile<EM>;
+    using H = HeadTile<TILE>;
     __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
     int tm, tn;
-    grouped_tile(xcd_contiguous_id(blockIdx.x, gridDim.x), cdiv(M, EM), cdiv(N, 256), 4, tm, tn);
-    dma::dma_tile<T, false, W_MN, 0, EM, 256, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
-        M, N, K, X, ldx, W, ldw, nullptr, 0, 1.0f, 0, tm * EM, tn * 256, lds, ex);
+    grouped_tile(xcd_contiguous_id(blockIdx.x, gridDim.x), cdiv(M, H::kEM), cdiv(N, H::kEN), 4, tm, tn);
+    dma::dma_tile<T, false, W_MN, 0, H::kEM, H::kEN, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
+        M, N, K, X, ldx, W, ldw, nullptr, 0, 1.0f, 0, tm * H::kEM, tn * H::kEN, lds, ex);
 }
 
 // dX's product over one of p.splits ranges of K: partial sums (EPI 0 or, adding to what is
 // there, 1), or the rounded result.
-template <typename T, bool B_MN, int EM, bool KR, int EPI>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EM == 64 ? 2 : 1)))
+template <typename T, bool B_MN, int TILE, bool KR, int EPI>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(HeadTile<TILE>::kPerSimd)))
 void xent_dx_kernel(ProductArgs p, int words) {
-    using H = HeadTile<EM>;
+    using H = HeadTile<TILE>;
+    constexpr int EM = H::kEM, EN = H::kEN;
     __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
-    const int tiles = cdiv(p.M, EM) * cdiv(p.N, 256);
+    const int tiles = cdiv(p.M, EM) * cdiv(p.N, EN);
     const int id = xcd_contiguous_id(blockIdx.x, gridDim.x);
     const int split = id / tiles;
     int tm, tn;
-    grouped_tile(id - split * tiles, cdiv(p.M, EM), cdiv(p.N, 256), 4, tm, tn);
+    grouped_tile(id - split * tiles, cdiv(p.M, EM), cdiv(p.N, EN), 4, tm, tn);
     const int k0 = split * p.step;
     const int K = split + 1 < p.splits ? p.step : p.K - k0;
     const uint16_t *A = p.A + k0, *B = p.B + (B_MN ? (size_t)k0 * p.ldb : (size_t)k0);
     if constexpr (EPI < 2) {
-        dma::dma_tile<T, false, B_MN, EPI, EM, 256, H::kWM, H::kWN, H::kNs, 0, false, KR>(
+        dma::dma_tile<T, false, B_MN, EPI, EM, EN, H::kWM, H::kWN, H::kNs, 0, false, KR>(
             p.rows, p.cols, K, A, p.lda, B, p.ldb, p.part + split * p.part_stride, p.ldo, 1.0f, EPI, tm * EM,
-            tn * 256, lds);
+            tn * EN, lds);
     } else {
         using EX = RoundEpilogue<T>;
-        dma::dma_tile<T, false, B_MN, 0, EM, 256, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
-            p.M, p.N, K, A, p.lda, B, p.ldb, nullptr, 0, 1.0f, 0, tm * EM, tn * 256, lds,
+        dma::dma_tile<T, false, B_MN, 0, EM, EN, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
+            p.M, p.N, K, A, p.lda, B, p.ldb, nullptr, 0, 1.0f, 0, tm * EM, tn * EN, lds,
             EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
     }
 }
@@ -278,57 +283,63 @@ void xent_dw_kernel(ProductArgs p, int words) {
         EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
 }
 
-template <typename T, bool W_MN, int EM, class EX>
+template <typename T, bool W_MN, int TILE, class EX>
 hipError_t launch_head_tile(const HeadArgs &h, const EX &ex, hipStream_t s) {
-    const dim3 grid(cdiv(h.M, EM) * cdiv(h.N, 256));
+    const dim3 grid(cdiv(h.M, kHeadRows[TILE]) * cdiv(h.N, kHeadCols[TILE]));
     const auto *X = (const uint16_t *)h.X, *W = (const uint16_t *)h.W;
-    if (h.K % 128 != 0)
-        hipLaunchKernelGGL((xent_head_kernel<T, W_MN, EM, true, EX>), grid, dim3(256), 0, s, h.M, h.N, h.K, X,
+    if (h.K % kHeadTrip[TILE] != 0)
+        hipLaunchKernelGGL((xent_head_kernel<T, W_MN, TILE, true, EX>), grid, dim3(256), 0, s, h.M, h.N, h.K, X,
                            h.ldx, W, h.ldw, ex);
     else
-        hipLaunchKernelGGL((xent_head_kernel<T, W_MN, EM, false, EX>), grid, dim3(256), 0, s, h.M, h.N, h.K, X,
+        hipLaunchKernelGGL((xent_head_kernel<T, W_MN, TILE, false, EX>), grid, dim3(256), 0, s, h.M, h.N, h.K, X,
                            h.ldx, W, h.ldw, ex);
     return hipGetLastError();
 }
 
-template <typename T, class EX>
-hipError_t launch_head(int em, const HeadArgs &h, const EX &ex, hipStream_t s) {
-    if (h.trans_b) {
-        if (em == 64) return launch_head_tile<T, false, 64>(h, ex, s);
-        if (em == 128) return launch_head_tile<T, false, 128>(h, ex, s);
-        return launch_head_tile<T, false, 256>(h, ex, s);
+template <typename T, bool W_MN, class EX>
+hipError_t launch_head_layout(int tile, const HeadArgs &h, const EX &ex, hipStream_t s) {
+    switch (tile) {
+    case kHead256: return launch_head_tile<T, W_MN, kHead256>(h, ex, s);
+    case kHead128: return launch_head_tile<T, W_MN, kHead128>(h, ex, s);
+    case kHead64: return launch_head_tile<T, W_MN, kHead64>(h, ex, s);
+    case kHead64x128: return launch_head_tile<T, W_MN, kHead64x128>(h, ex, s);
+    default: return launch_head_tile<T, W_MN, kHead64x64>(h, ex, s);
     }
-    if (em == 64) return launch_head_tile<T, true, 64>(h, ex, s);
-    if (em == 128) return launch_head_tile<T, true, 128>(h, ex, s);
-    return launch_head_tile<T, true, 256>(h, ex, s);
+}
+
+template <typename T, class EX>
+hipError_t launch_head(int tile, const HeadArgs &h, const EX &ex, hipStream_t s) {
+    return h.trans_b ? launch_head_layout<T, false>(tile, h, ex, s) : launch_head_layout<T, true>(tile, h, ex, s);
 }
 
 inline int word_stores(const ProductArgs &p) { return p.ldo % 2 == 0 && (uintptr_t)p.out % 4 == 0; }
 
-template <typename T, bool B_MN, int EM, bool KR>
+template <typename T, bool B_MN, int TILE, bool KR>
 hipError_t launch_dx_epi(const ProductArgs &p, hipStream_t s) {
-    const dim3 grid(cdiv(p.M, EM) * cdiv(p.N, 256) * p.splits);
+    const dim3 grid(cdiv(p.M, kHeadRows[TILE]) * cdiv(p.N, kHeadCols[TILE]) * p.splits);
     if (p.part == nullptr)
-        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, EM, KR, 2>), grid, dim3(256), 0, s, p, word_stores(p));
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 2>), grid, dim3(256), 0, s, p, word_stores(p));
     else if (p.accumulate)
-        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, EM, KR, 1>), grid, dim3(256), 0, s, p, 0);
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 1>), grid, dim3(256), 0, s, p, 0);
     else
-        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, EM, KR, 0>), grid, dim3(256), 0, s, p, 0);
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 0>), grid, dim3(256), 0, s, p, 0);
     return hipGetLastError();
 }
 
 template <typename T, bool B_MN>
-hipError_t launch_dx_layout(int em, const ProductArgs &p, hipStream_t s) {
+hipError_t launch_dx_layout(int tile, const ProductArgs &p, hipStream_t s) {
     // the ranges before the last are whole ring trips
     const bool kr = p.K % 128 != 0;
-    if (em == 64) return kr ? launch_dx_epi<T, B_MN, 64, true>(p, s) : launch_dx_epi<T, B_MN, 64, false>(p, s);
-    if (em == 128) return kr ? launch_dx_epi<T, B_MN, 128, true>(p, s) : launch_dx_epi<T, B_MN, 128, false>(p, s);
-    return kr ? launch_dx_epi<T, B_MN, 256, true>(p, s) : launch_dx_epi<T, B_MN, 256, false>(p, s);
+    if (tile == kHead64)
+        return kr ? launch_dx_epi<T, B_MN, kHead64, true>(p, s) : launch_dx_epi<T, B_MN, kHead64, false>(p, s);
+    if (tile == kHead128)
+        return kr ? launch_dx_epi<T, B_MN, kHead128, true>(p, s) : launch_dx_epi<T, B_MN, kHead128, false>(p, s);
+    return kr ? launch_dx_epi<T, B_MN, kHead256, true>(p, s) : launch_dx_epi<T, B_MN, kHead256, false>(p, s);
 }
 
 template <typename T>
-hipError_t launch_dx(int em, bool b_mn, const ProductArgs &p, hipStream_t s) {
-    return b_mn ? launch_dx_layout<T, true>(em, p, s) : launch_dx_layout<T, false>(em, p, s);
+hipError_t launch_dx(int tile, bool b_mn, const ProductArgs &p, hipStream_t s) {
+    return b_mn ? launch_dx_layout<T, true>(tile, p, s) : launch_dx_layout<T, false>(tile, p, s);
 }
 
 template <typename T>

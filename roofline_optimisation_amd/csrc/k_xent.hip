@@ -10,6 +10,8 @@
 //
 // This file: the rows' kernels, the plan that lays out a call's workspace, and the entry
 // points.  The products run in this library's GEMM kernels.
+#include <algorithm>
+
 #include "../../include/gemm355_softmax.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -132,11 +134,19 @@ __global__ __launch_bounds__(1024) void xent_merge_kernel(int M, int N, int bloc
     finish_row(row, m, l, label >= 0 && label < N ? zl[row] : 0.0f, label, ignore, N, loss, lse);
 }
 
-// X's rows copied to rows of ldm elements, zeros after the K-th.
-__global__ __launch_bounds__(256) void xent_copy_kernel(int K, const uint16_t *__restrict__ X, int ldx, uint16_t *Xm,
-                                                        int ldm) {
-    for (int c = threadIdx.x; c < ldm; c += 256)
-        Xm[(size_t)blockIdx.x * ldm + c] = c < K ? X[(size_t)blockIdx.x * ldx + c] : (uint16_t)0;
+// src (rows x cols, row stride lds, any alignment) copied to aligned rows of ldd elements (a
+// multiple of 8), zeros past the last column and in the rows from `rows` to `all`.  Grid: (16-
+// byte chunks of a row / 256, all).
+__global__ __launch_bounds__(256) void xent_copy_kernel(int rows, int cols, const uint16_t *__restrict__ src, int lds,
+                                                        uint16_t *dst, int ldd) {
+    const int c = 8 * (blockIdx.x * 256 + (int)threadIdx.x), r = blockIdx.y;
+    if (c >= ldd) return;
+    const uint16_t *x = src + (size_t)r * lds + c;
+    u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (r < rows && c + 8 <= cols) v = *(const u16x8_ua *)x;
+    else if (r < rows)
+        for (int i = 0; i < 8 && c + i < cols; ++i) v[i] = x[i];
+    *(u16x8 *)(dst + (size_t)r * ldd + c) = v;
 }
 
 // Before the gradient's pieces: scale[0] = S and scale[1] = 1 / S (S = 1 unless `rescale`:
@@ -323,19 +333,23 @@ struct GradPlan {
     }
 };
 
-// Whether the matrix-core tiles with fused epilogues take these shapes: 16-bit types, K a
-// multiple of 8 of at least one ring trip, and more classes than one tile has.
-bool fused_shape(int dtype, unsigned flags, int N, int K) {
-    return dtype != kF32 && K % 8 == 0 && K >= 128 && N >= 256 && (flags & GEMM355_TRANS_B || N % 8 == 0);
-}
+// Whether the matrix-core tiles with fused epilogues take these shapes: 16-bit types, as many
+// classes as a product over them needs for a ring trip and more, and 256 rows of K within the
+// range of a tile's offsets.
+bool fused_shape(int dtype, int N, int K) { return dtype != kF32 && N >= 256 && K <= 1 << 20; }
+
+// The hidden size the tiles work with: whole 16-byte chunks, a ring trip at least.
+int padded_hidden(int K) { return (int)up((size_t)(K < 128 ? 128 : K), 8); }
 
 // Byte offsets of `rows` rows of stride ld (and the ring trip past them) below 2^31.
 bool offsets_fit(long rows, long ld) { return (rows + 256) * ld * 2 < (1L << 31); }
 
-// Whether W's rows can be loaded by them: 16-byte aligned, and offsets within a tile (TRANS_B)
-// or of all K rows in range.
-bool fused_weights(unsigned flags, int K, const void *W, int ldw) {
-    return rows_aligned16(W, ldw, 2) && offsets_fit(flags & GEMM355_TRANS_B ? 256 : K, ldw);
+// Whether the tiles can load W where it lies: rows of whole chunks, 16-byte aligned, offsets
+// within a tile (TRANS_B) or of all K rows in range.  Else each piece of it is copied to the
+// workspace first.
+bool weights_load(unsigned flags, int N, int K, const void *W, int ldw) {
+    return K == padded_hidden(K) && (flags & GEMM355_TRANS_B || N % 8 == 0) && rows_aligned16(W, ldw, 2) &&
+           offsets_fit(flags & GEMM355_TRANS_B ? 256 : K, ldw);
 }
 
 // The time of M x N logits in one kind of tile, in rounds of 256 x 256 tiles (one per CU):
@@ -405,23 +419,41 @@ int stat_blocks(const Section &c) {
     return cdiv(c.cols, kHeadCols[c.tile]) * (kHeadCols[c.tile] / kStatCols[c.tile]);
 }
 
+constexpr long kCopyBytes = 1L << 27;  // of W at once, where it has to be copied
+
+// Columns of a piece: a multiple of 256, at most `fit` (but at least 256), the last piece not
+// below 256 either unless it is the only one.
+int even_pieces(int N, long fit) {
+    fit = fit < 256 ? 256 : fit / 256 * 256;
+    const int pieces = (int)((N + fit - 1) / fit);
+    int cols = (int)up((size_t)cdiv(N, pieces), 256);
+    while (cols < N && N % cols != 0 && N % cols < 256) cols += 256;
+    return cols;
+}
+
 struct FusedForwardPlan {
-    int rows, blocks, ldm, sections;
-    Section section[2];
+    int rows, cols, blocks, Kp, ldw;
     float2 *part;
     float *zl;
-    uint16_t *Xm;
+    uint16_t *Xm, *Wm;
     size_t bytes;
-    FusedForwardPlan(int M, int N, int K, void *ws) {
+    // copied: W is copied, `cols` classes at a time
+    FusedForwardPlan(bool copied, unsigned flags, int M, int N, int K, void *ws) {
         rows = M < kStatRows ? M : kStatRows;
-        sections = head_sections(rows, N, K, section);
+        Kp = padded_hidden(K);
+        cols = copied ? even_pieces(N, kCopyBytes / 2 / Kp) : N;
+        ldw = flags & GEMM355_TRANS_B ? Kp : (int)up((size_t)cols, 8);
         blocks = 0;
-        for (int i = 0; i < sections; ++i) blocks += stat_blocks(section[i]);
-        ldm = K;
+        for (int v0 = 0; v0 < N; v0 += cols) {
+            Section part[2];
+            const int n = head_sections(rows, N - v0 < cols ? N - v0 : cols, Kp, part);
+            for (int i = 0; i < n; ++i) blocks += stat_blocks(part[i]);
+        }
         Carver c{(char *)ws};
         part = (float2 *)c.take((size_t)blocks * rows * sizeof(float2));
         zl = (float *)c.take((size_t)rows * 4);
-        Xm = (uint16_t *)c.take((size_t)rows * ldm * 2);
+        Xm = (uint16_t *)c.take((size_t)rows * Kp * 2);
+        Wm = (uint16_t *)c.take(copied ? (size_t)(flags & GEMM355_TRANS_B ? cols : Kp) * ldw * 2 : 0);
         bytes = c.used;
     }
 };
@@ -442,28 +474,31 @@ struct Splits {
 constexpr long kDzBytes = 1L << 29;  // dZ of a piece
 
 struct FusedGradPlan {
-    int cols, Mp, ldm, dx, splits;
+    int cols, Mp, Kp, ldw, dx, splits, ldx;
     float *scale, *dX;
     RowGrad *rows;
-    uint16_t *Xm, *dZ;
-    size_t bytes;
-    FusedGradPlan(int M, int N, int K, void *ws) {
+    uint16_t *Xm, *dZ, *Wm;
+    size_t dx_stride, bytes;
+    FusedGradPlan(bool copied, unsigned flags, int M, int N, int K, void *ws) {
         Mp = (int)up((size_t)M, 128);  // whole ring trips of dW's product, zeros past M
-        ldm = K;
+        Kp = padded_hidden(K);
         dx = dx_tile(M);
-        const long fit = kDzBytes / 2 / Mp / 256 * 256;
-        const int pieces = (int)((N + (fit < 256 ? 256 : fit) - 1) / (fit < 256 ? 256 : fit));
-        cols = (int)up((size_t)cdiv(N, pieces), 256);
-        while (cols < N && N % cols != 0 && N % cols < 256) cols += 256;
+        long fit = kDzBytes / 2 / Mp;
+        if (copied && kCopyBytes / 2 / Kp < fit) fit = kCopyBytes / 2 / Kp;
+        cols = even_pieces(N, fit);
+        ldw = flags & GEMM355_TRANS_B ? Kp : cols;
         // dX's product: as many ranges of a piece's classes as fill the 256 CUs
         const int nc = cols < N ? cols : N;
         splits = Splits(nc, 256 / (cdiv(M, kHeadRows[dx]) * cdiv(K, kHeadCols[dx]))).count;
+        ldx = (int)up((size_t)K, 4);
+        dx_stride = (size_t)M * ldx;
         Carver c{(char *)ws};
         scale = (float *)c.take(8);
         rows = (RowGrad *)c.take((size_t)Mp * sizeof(RowGrad));
-        Xm = (uint16_t *)c.take((size_t)Mp * ldm * 2);
+        Xm = (uint16_t *)c.take((size_t)Mp * Kp * 2);
         dZ = (uint16_t *)c.take((size_t)Mp * cols * 2);
-        dX = (float *)c.take((size_t)splits * M * K * 4);
+        dX = (float *)c.take((size_t)splits * dx_stride * 4);
+        Wm = (uint16_t *)c.take(copied ? (size_t)(flags & GEMM355_TRANS_B ? cols : Kp) * ldw * 2 : 0);
         bytes = c.used;
     }
 };
@@ -498,39 +533,65 @@ gemm355_status status_of(hipError_t e) { return e == hipSuccess ? GEMM355_OK : G
         if (try_e != hipSuccess) return GEMM355_ERR_LAUNCH; \
     } while (0)
 
-hipError_t merge(int M, int N, const FusedForwardPlan &p, const int64_t *labels, int64_t ignore, float *loss,
+hipError_t merge(int M, int N, int blocks, const FusedForwardPlan &p, const int64_t *labels, int64_t ignore, float *loss,
                  float *lse, hipStream_t s) {
     if (M >= 32)
-        hipLaunchKernelGGL((xent_merge_kernel<32>), dim3(cdiv(M, 32)), dim3(1024), 0, s, M, N, p.blocks, p.part,
+        hipLaunchKernelGGL((xent_merge_kernel<32>), dim3(cdiv(M, 32)), dim3(1024), 0, s, M, N, blocks, p.part,
                            p.rows, p.zl, labels, ignore, loss, lse);
     else
-        hipLaunchKernelGGL((xent_merge_kernel<4>), dim3(cdiv(M, 4)), dim3(1024), 0, s, M, N, p.blocks, p.part,
+        hipLaunchKernelGGL((xent_merge_kernel<4>), dim3(cdiv(M, 4)), dim3(1024), 0, s, M, N, blocks, p.part,
                            p.rows, p.zl, labels, ignore, loss, lse);
     return hipGetLastError();
+}
+
+hipError_t copy_rows(int rows, int all, int cols, const void *src, int lds, uint16_t *dst, int ldd, hipStream_t s) {
+    return over_rows(all, [&](int r, int n) {
+        hipLaunchKernelGGL(xent_copy_kernel, dim3(cdiv(ldd / 8, 256), n), dim3(256), 0, s, rows - r, cols,
+                           (const uint16_t *)src + (size_t)r * lds, lds, dst + (size_t)r * ldd, ldd);
+    });
+}
+
+// The piece of W from class v0 on, nc classes, copied: K x nc or nc x K to aligned rows,
+// zeros from K to Kp.
+hipError_t copy_weights(unsigned flags, int nc, int K, int Kp, const void *w, int ldw, uint16_t *Wm, int ldm,
+                        hipStream_t s) {
+    if (flags & GEMM355_TRANS_B) return copy_rows(nc, nc, K, w, ldw, Wm, ldm, s);
+    return copy_rows(K, Kp, nc, w, ldw, Wm, ldm, s);
 }
 
 gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
                              int ldw, const int64_t *labels, int64_t ignore, float *loss, float *lse, void *ws,
                              hipStream_t s) {
-    const FusedForwardPlan p(M, N, K, ws);
-    const bool copy = !rows_aligned16(X, ldx, 2) || !offsets_fit(256, ldx);
+    const bool copied = !weights_load(flags, N, K, W, ldw), tb = flags & GEMM355_TRANS_B;
+    const FusedForwardPlan p(copied, flags, M, N, K, ws);
+    const bool copy_x = K != p.Kp || !rows_aligned16(X, ldx, 2) || !offsets_fit(256, ldx);
     for (int r0 = 0; r0 < M; r0 += p.rows) {
         const int rows = M - r0 < p.rows ? M - r0 : p.rows;
         const void *x = at(X, (size_t)r0 * ldx, 2);
-        if (copy) {
-            hipLaunchKernelGGL(xent_copy_kernel, dim3(rows), dim3(256), 0, s, K, (const uint16_t *)x, ldx, p.Xm, p.ldm);
-            G355_TRY(hipGetLastError());
-        }
+        if (copy_x) G355_TRY(copy_rows(rows, rows, K, x, ldx, p.Xm, p.Kp, s));
         float2 *part = p.part;
-        for (int i = 0; i < p.sections; ++i) {
-            const Section &c = p.section[i];
-            const HeadArgs h{rows, c.cols, K, copy ? p.Xm : x, copy ? p.ldm : ldx, at(W, w_offset(flags, c.v0, ldw), 2),
-                             ldw, (flags & GEMM355_TRANS_B) != 0};
-            G355_TRY(dtype == kF16 ? launch_xent_stats_f16(c.tile, h, labels + r0, c.v0, part, p.rows, p.zl, s)
-                                   : launch_xent_stats_bf16(c.tile, h, labels + r0, c.v0, part, p.rows, p.zl, s));
-            part += (size_t)stat_blocks(c) * p.rows;
+        int blocks = 0;
+        for (int v0 = 0; v0 < N; v0 += p.cols) {
+            const int nc = N - v0 < p.cols ? N - v0 : p.cols;
+            const void *w = at(W, w_offset(flags, v0, ldw), 2);
+            if (copied) G355_TRY(copy_weights(flags, nc, K, p.Kp, w, ldw, p.Wm, p.ldw, s));
+            if (copied) w = p.Wm;
+            const int lw = copied ? p.ldw : ldw;
+            Section sec[2];
+            const int n = head_sections(rows, nc, p.Kp, sec);
+            for (int i = 0; i < n; ++i) {
+                const Section &c = sec[i];
+                const HeadArgs h{rows, c.cols, p.Kp, copy_x ? p.Xm : x, copy_x ? p.Kp : ldx,
+                                 at(w, w_offset(flags, c.v0, lw), 2), lw, tb};
+                G355_TRY(dtype == kF16
+                             ? launch_xent_stats_f16(c.tile, h, labels + r0, v0 + c.v0, part, p.rows, p.zl, s)
+                             : launch_xent_stats_bf16(c.tile, h, labels + r0, v0 + c.v0, part, p.rows, p.zl, s));
+                part += (size_t)stat_blocks(c) * p.rows;
+                blocks += stat_blocks(c);
+            }
         }
-        G355_TRY(merge(rows, N, p, labels + r0, ignore, loss ? loss + r0 : nullptr, lse ? lse + r0 : nullptr, s));
+        G355_TRY(merge(rows, N, blocks, p, labels + r0, ignore, loss ? loss + r0 : nullptr, lse ? lse + r0 : nullptr,
+                       s));
     }
     return GEMM355_OK;
 }
@@ -620,19 +681,22 @@ hipError_t round16(const GradCall &a, int rows, int cols, const float *acc, int 
     });
 }
 
-gemm355_status gradient_fused(const GradCall &a, void *ws) {
-    const FusedGradPlan p(a.M, a.N, a.K, ws);
+gemm355_status gradient_fused(const GradCall &a, bool copied, void *ws) {
+    const FusedGradPlan p(copied, a.flags, a.M, a.N, a.K, ws);
     const bool tb = a.flags & GEMM355_TRANS_B, f16 = a.dtype == kF16;
-    G355_TRY(prep(a, p.Mp, p.scale, p.rows, p.Xm, p.ldm));
+    G355_TRY(prep(a, p.Mp, p.scale, p.rows, p.Xm, p.Kp));
     const bool one = p.cols >= a.N && p.splits == 1;  // dX in one product
     for (int v0 = 0; v0 < a.N; v0 += p.cols) {
         const int nc = a.N - v0 < p.cols ? a.N - v0 : p.cols;
         const auto *w = (const uint16_t *)at(a.W, w_offset(a.flags, v0, a.ldw), 2);
+        if (copied) G355_TRY(copy_weights(a.flags, nc, a.K, p.Kp, w, a.ldw, p.Wm, p.ldw, a.s));
+        if (copied) w = p.Wm;
+        const int lw = copied ? p.ldw : a.ldw;
         Section part[2];
-        const int dz_parts = head_sections(p.Mp, nc, a.K, part);
+        const int dz_parts = head_sections(p.Mp, nc, p.Kp, part);
         for (int i = 0; i < dz_parts; ++i) {
             const Section &c = part[i];
-            const HeadArgs h{p.Mp, c.cols, a.K, p.Xm, p.ldm, w + w_offset(a.flags, c.v0, a.ldw), a.ldw, tb};
+            const HeadArgs h{p.Mp, c.cols, p.Kp, p.Xm, p.Kp, w + w_offset(a.flags, c.v0, lw), lw, tb};
             uint16_t *dZ = p.dZ + c.v0;
             G355_TRY(f16 ? launch_xent_dz_f16(c.tile, h, p.rows, v0 + c.v0, dZ, p.cols, a.s)
                          : launch_xent_dz_bf16(c.tile, h, p.rows, v0 + c.v0, dZ, p.cols, a.s));
@@ -641,12 +705,13 @@ gemm355_status gradient_fused(const GradCall &a, void *ws) {
             const Splits sp(nc, p.splits);
             ProductArgs q{};
             q.M = q.rows = a.M;
-            q.N = q.cols = a.K;
+            q.N = p.Kp;
+            q.cols = a.K;
             q.K = nc;
             q.A = p.dZ;
             q.lda = p.cols;
             q.B = w;
-            q.ldb = a.ldw;
+            q.ldb = lw;
             q.splits = sp.count;
             q.step = sp.step;
             if (one) {
@@ -655,8 +720,8 @@ gemm355_status gradient_fused(const GradCall &a, void *ws) {
                 q.factor = p.scale + 1;
             } else {
                 q.part = p.dX;
-                q.part_stride = (size_t)a.M * a.K;
-                q.ldo = a.K;
+                q.part_stride = p.dx_stride;
+                q.ldo = p.ldx;
                 q.accumulate = v0 > 0;
             }
             G355_TRY(f16 ? launch_xent_dx_f16(p.dx, tb, q, a.s) : launch_xent_dx_bf16(p.dx, tb, q, a.s));
@@ -669,11 +734,11 @@ gemm355_status gradient_fused(const GradCall &a, void *ws) {
             ProductArgs q{};
             q.K = p.Mp;
             q.A = tb ? dZ : p.Xm;
-            q.lda = tb ? p.cols : p.ldm;
+            q.lda = tb ? p.cols : p.Kp;
             q.B = tb ? p.Xm : dZ;
-            q.ldb = tb ? p.ldm : p.cols;
-            q.M = tb ? padded : a.K;
-            q.N = tb ? a.K : padded;
+            q.ldb = tb ? p.Kp : p.cols;
+            q.M = tb ? padded : p.Kp;
+            q.N = tb ? p.Kp : padded;
             q.rows = tb ? c.cols : a.K;
             q.cols = tb ? a.K : c.cols;
             q.out = (uint16_t *)at(a.dW, w_offset(a.flags, v0 + c.v0, a.lddw), 2);
@@ -683,16 +748,17 @@ gemm355_status gradient_fused(const GradCall &a, void *ws) {
         }
     }
     if (!one && a.dX != nullptr)
-        G355_TRY(round16(a, a.M, a.K, p.dX, a.K, p.splits, (size_t)a.M * a.K, p.scale, a.dX, a.lddx));
+        G355_TRY(round16(a, a.M, a.K, p.dX, p.ldx, p.splits, p.dx_stride, p.scale, a.dX, a.lddx));
     return GEMM355_OK;
 }
 
 // Whether the fused gradient takes this call: every operand's offsets in range.
-bool fused_gradient(const GradCall &a) {
-    if (!fused_shape(a.dtype, a.flags, a.N, a.K) || !fused_weights(a.flags, a.K, a.W, a.ldw)) return false;
-    const FusedGradPlan p(a.M, a.N, a.K, nullptr);
-    return offsets_fit(p.Mp, p.cols) && offsets_fit(p.Mp, p.ldm) &&
-           (!(a.flags & GEMM355_TRANS_B) || offsets_fit(p.cols, a.ldw));
+bool fused_gradient(const GradCall &a, bool copied) {
+    if (!fused_shape(a.dtype, a.N, a.K)) return false;
+    const FusedGradPlan p(copied, a.flags, a.M, a.N, a.K, nullptr);
+    return offsets_fit(p.Mp, p.cols) && offsets_fit(p.Mp, p.Kp) &&
+           (!(a.flags & GEMM355_TRANS_B) || offsets_fit(p.cols, copied ? p.ldw : a.ldw)) &&
+           (!copied || offsets_fit(p.Kp, p.ldw));
 }
 
 gemm355_status gradient(const GradCall &a, void *ws) {
@@ -749,9 +815,10 @@ extern "C" {
 size_t gemm355_xent_workspace(int dtype, unsigned flags, int M, int N, int K) {
     if (!valid_shape(dtype, flags, M, N, K) || M == 0) return 0;
     const size_t any = ForwardPlan(M, N, nullptr).bytes;
-    if (!fused_shape(dtype, flags, N, K)) return any;
-    const size_t fused = FusedForwardPlan(M, N, K, nullptr).bytes;
-    return fused > any ? fused : any;  // which one runs depends on W's alignment
+    if (!fused_shape(dtype, N, K)) return any;
+    // which one runs depends on W's alignment
+    return std::max({any, FusedForwardPlan(false, flags, M, N, K, nullptr).bytes,
+                     FusedForwardPlan(true, flags, M, N, K, nullptr).bytes});
 }
 
 gemm355_status gemm355_xent(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
@@ -776,17 +843,16 @@ gemm355_status gemm355_xent(int dtype, unsigned flags, int M, int N, int K, cons
             if (out[i].meets(out[j])) return GEMM355_ERR_INVALID_ARG;
     }
     if (!current_device_is_gfx950()) return GEMM355_ERR_DEVICE;
-    const bool fused = fused_shape(dtype, flags, N, K) && fused_weights(flags, K, W, ldw);
-    return (fused ? forward_fused : forward)(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, lse,
-                                             workspace, stream);
+    return (fused_shape(dtype, N, K) ? forward_fused : forward)(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, lse,
+                                                             workspace, stream);
 }
 
 size_t gemm355_xent_grad_workspace(int dtype, unsigned flags, int M, int N, int K) {
     if (!valid_shape(dtype, flags, M, N, K) || M == 0) return 0;
     const size_t any = GradPlan(dtype, M, N, K, nullptr).bytes;
-    if (!fused_shape(dtype, flags, N, K)) return any;
-    const size_t fused = FusedGradPlan(M, N, K, nullptr).bytes;
-    return fused > any ? fused : any;
+    if (!fused_shape(dtype, N, K)) return any;
+    return std::max({any, FusedGradPlan(false, flags, M, N, K, nullptr).bytes,
+                     FusedGradPlan(true, flags, M, N, K, nullptr).bytes});
 }
 
 gemm355_status gemm355_xent_grad(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx,
@@ -833,7 +899,8 @@ gemm355_status gemm355_xent_grad(int dtype, unsigned flags, int M, int N, int K,
                                    (uint16_t *)dW + (size_t)r * lddw, lddw);
         }));
     const GradCall a{dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, lse, dloss, dX, lddx, dW, lddw, stream};
-    return fused_gradient(a) ? gradient_fused(a, workspace) : gradient(a, workspace);
+    const bool copied = !weights_load(flags, N, K, W, ldw);
+    return fused_gradient(a, copied) ? gradient_fused(a, copied, workspace) : gradient(a, workspace);
 }
 
 }  // extern "C"

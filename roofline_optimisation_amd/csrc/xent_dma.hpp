@@ -218,6 +218,21 @@ struct RoundEpilogue {
     }
 };
 
+// Binary32 partial sums, stored (EPI 0) or added to what is there (EPI 1).
+template <typename T, int EPI>
+struct PartialEpilogue {
+    int nrows, ncols;
+    float *part;
+    int ldo;
+    __device__ int rows() const { return nrows; }
+    __device__ int cols() const { return ncols; }
+
+    template <bool EDGE, int kMB, int kNB>
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+        dma::store_tile<EPI, T, EDGE>(acc, part, ldo, row0, col0, nrows, ncols, 1.0f, EPI);
+    }
+};
+
 // The tiles' waves and ring stages: 256 x 256 on 2 x 2 waves of 128 x 128, 128 x 256 on 2 x 2
 // of 64 x 128, 64 x 256 on 1 x 4 of 64 x 64, 64 x 128 and 64 x 64 on 2 x 2.
 template <int TILE>
@@ -238,8 +253,9 @@ void xent_head_kernel(int M, int N, int K, const uint16_t *__restrict__ X, int l
     __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
     int tm, tn;
     grouped_tile(xcd_contiguous_id(blockIdx.x, gridDim.x), cdiv(M, H::kEM), cdiv(N, H::kEN), 4, tm, tn);
+    // a K x N W is loaded in whole chunks of 8 classes; what lies past N in the last is masked
     dma::dma_tile<T, false, W_MN, 0, H::kEM, H::kEN, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
-        M, N, K, X, ldx, W, ldw, nullptr, 0, 1.0f, 0, tm * H::kEM, tn * H::kEN, lds, ex);
+        M, W_MN ? (N + 7) & ~7 : N, K, X, ldx, W, ldw, nullptr, 0, 1.0f, 0, tm * H::kEM, tn * H::kEN, lds, ex);
 }
 
 // dX's product over one of p.splits ranges of K: partial sums (EPI 0 or, adding to what is
@@ -250,18 +266,19 @@ void xent_dx_kernel(ProductArgs p, int words) {
     using H = HeadTile<TILE>;
     constexpr int EM = H::kEM, EN = H::kEN;
     __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
-    const int tiles = cdiv(p.M, EM) * cdiv(p.N, EN);
+    const int tiles = cdiv(p.rows, EM) * cdiv(p.cols, EN);
     const int id = xcd_contiguous_id(blockIdx.x, gridDim.x);
     const int split = id / tiles;
     int tm, tn;
-    grouped_tile(id - split * tiles, cdiv(p.M, EM), cdiv(p.N, EN), 4, tm, tn);
+    grouped_tile(id - split * tiles, cdiv(p.rows, EM), cdiv(p.cols, EN), 4, tm, tn);
     const int k0 = split * p.step;
     const int K = split + 1 < p.splits ? p.step : p.K - k0;
     const uint16_t *A = p.A + k0, *B = p.B + (B_MN ? (size_t)k0 * p.ldb : (size_t)k0);
     if constexpr (EPI < 2) {
-        dma::dma_tile<T, false, B_MN, EPI, EM, EN, H::kWM, H::kWN, H::kNs, 0, false, KR>(
-            p.rows, p.cols, K, A, p.lda, B, p.ldb, p.part + split * p.part_stride, p.ldo, 1.0f, EPI, tm * EM,
-            tn * EN, lds);
+        using EX = PartialEpilogue<T, EPI>;
+        dma::dma_tile<T, false, B_MN, 0, EM, EN, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
+            p.M, p.N, K, A, p.lda, B, p.ldb, nullptr, 0, 1.0f, 0, tm * EM, tn * EN, lds,
+            EX{p.rows, p.cols, p.part + split * p.part_stride, p.ldo});
     } else {
         using EX = RoundEpilogue<T>;
         dma::dma_tile<T, false, B_MN, 0, EM, EN, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
@@ -316,7 +333,7 @@ inline int word_stores(const ProductArgs &p) { return p.ldo % 2 == 0 && (uintptr
 
 template <typename T, bool B_MN, int TILE, bool KR>
 hipError_t launch_dx_epi(const ProductArgs &p, hipStream_t s) {
-    const dim3 grid(cdiv(p.M, kHeadRows[TILE]) * cdiv(p.N, kHeadCols[TILE]) * p.splits);
+    const dim3 grid(cdiv(p.rows, kHeadRows[TILE]) * cdiv(p.cols, kHeadCols[TILE]) * p.splits);
     if (p.part == nullptr)
         hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 2>), grid, dim3(256), 0, s, p, word_stores(p));
     else if (p.accumulate)

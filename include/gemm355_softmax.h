@@ -94,7 +94,8 @@ size_t gemm355_xent_workspace(int dtype, unsigned flags, int M, int N, int K);
  *
  * Error of lse_t against the exact value of the given operands: the error e of a binary32
  * dot product of length K (as for gemm_f32 and its 16-bit counterparts) plus about
- * 2^-24 (4 |lse_t| + N / 256 + 64). */
+ * 2^-24 (4 |lse_t| + N / 256 + 64).  A logit that is NaN, +infinity, or 2^127 or more in
+ * magnitude makes its row's results NaN. */
 gemm355_status gemm355_xent(int dtype, unsigned flags, int M, int N, int K, const void *X,
                             int ldx, const void *W, int ldw, const int64_t *labels,
                             int64_t ignore, float *loss, float *lse, void *workspace,

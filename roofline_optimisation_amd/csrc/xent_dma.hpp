@@ -13,19 +13,29 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Maximum and sum over the 16 lanes that hold a row of a 16 x 16 accumulator quad; every
-// one of them gets the result.
+// Another lane's value within the 16 lanes that hold a row of a 16 x 16 accumulator quad.
+template <int CTRL>
+__device__ __forceinline__ float of_lane(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+// The larger of two values; as the median with +infinity it costs one instruction, where
+// fmaxf first quiets operands that could be signalling.  A NaN operand gives either value.
+__device__ __forceinline__ float max2(float a, float b) {
+    return __builtin_amdgcn_fmed3f(a, b, __builtin_huge_valf());
+}
+
+// Maximum and sum over those 16 lanes; every one of them gets the result.
 __device__ __forceinline__ float row16_max(float v) {
-    v = fmaxf(v, DppXchg<kDppQuadXor1>::get(v));
-    v = fmaxf(v, DppXchg<kDppQuadXor2>::get(v));
-    v = fmaxf(v, DppXchg<kDppRowHalfMirror>::get(v));
-    return fmaxf(v, DppXchg<kDppRowMirror>::get(v));
+    v = max2(v, of_lane<kDppQuadXor1>(v));
+    v = max2(v, of_lane<kDppQuadXor2>(v));
+    v = max2(v, of_lane<kDppRowHalfMirror>(v));
+    return max2(v, of_lane<kDppRowMirror>(v));
 }
 __device__ __forceinline__ float row16_sum(float v) {
-    v += DppXchg<kDppQuadXor1>::get(v);
-    v += DppXchg<kDppQuadXor2>::get(v);
-    v += DppXchg<kDppRowHalfMirror>::get(v);
-    return v + DppXchg<kDppRowMirror>::get(v);
+    v += of_lane<kDppQuadXor1>(v);
+    v += of_lane<kDppQuadXor2>(v);
+    v += of_lane<kDppRowHalfMirror>(v);
+    return v + of_lane<kDppRowMirror>(v);
 }
 
 // An accumulator register, read where it is used (left to itself the compiler copies all 256
@@ -80,34 +90,49 @@ struct StatsEpilogue {
                 }
                 if (i + 1 < kMB) load_labels(i + 1);
                 __builtin_amdgcn_sched_barrier(0);
+                // the four rows in straight-line code, so that their chains of dependent
+                // instructions overlap: with one wave per SIMD nothing else does
+                float x[4][kNB], m[4], l[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float x[kNB];
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int j = 0; j < kNB; ++j) {
-                        x[j] = acc_read(acc[i][j][r]);
-                        if (EDGE && col0 + 16 * j + c16 >= N) x[j] = kNegInf;
+                        x[r][j] = acc_read(acc[i][j][r]);
+                        if (EDGE && col0 + 16 * j + c16 >= N) x[r][j] = kNegInf;
                     }
-                    // the label's logit (of a row of many columns few tiles hold the label's)
-                    if (__any(rel[r] >= 0)) {
+                // the labels' logits (of rows of many columns few tiles hold any label's)
+                if (__any(max(max(rel[0], rel[1]), max(rel[2], rel[3])) >= 0)) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
 #pragma unroll
                         for (int j = 0; j < kNB; ++j)
-                            if (rel[r] == 16 * j + c16) zl[r0 + r] = x[j];
-                    }
-                    float m = x[0];
-#pragma unroll
-                    for (int j = 1; j < kNB; ++j) m = fmaxf(m, x[j]);
-                    m = row16_max(m);
-                    const float shift = m == kNegInf ? 0.0f : m;
-                    float l = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < kNB; ++j) l += __builtin_amdgcn_exp2f((x[j] - shift) * kLog2e);
-                    l = row16_sum(l);
-                    if (c16 == 4 * ii + r) {
-                        km = m;
-                        kl = l;
-                    }
+                            if (rel[r] == 16 * j + c16) zl[r0 + r] = x[r][j];
                 }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    m[r] = x[r][0];
+#pragma unroll
+                    for (int j = 1; j < kNB; ++j) m[r] = max2(m[r], x[r][j]);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) m[r] = row16_max(m[r]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    // exp(x - m) as 2^(x log2 e - m log2 e): the rounding of m log2 e moves all of
+                    // the sum by |m| 2^-24 of it
+                    const float shift = m[r] == kNegInf ? 0.0f : -m[r] * kLog2e;
+                    l[r] = __builtin_amdgcn_exp2f(fmaf(x[r][0], kLog2e, shift));
+#pragma unroll
+                    for (int j = 1; j < kNB; ++j) l[r] += __builtin_amdgcn_exp2f(fmaf(x[r][j], kLog2e, shift));
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) l[r] = row16_sum(l[r]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (c16 == 4 * ii + r) {
+                        km = m[r];
+                        kl = l[r];
+                    }
             }
             const int row = row0 + 16 * (g + (c16 >> 2)) + 4 * q4 + (c16 & 3);
             if (c16 < 4 * kI && (!EDGE || row < M)) out[row] = make_float2(km, kl);
@@ -120,7 +145,7 @@ struct StatsEpilogue {
 // those of the second.
 template <typename T>
 __device__ __forceinline__ uint32_t pair_word(float a0, float a1, int odd) {
-    const float other = DppXchg<kDppQuadXor1>::get(odd ? a0 : a1);
+    const float other = of_lane<kDppQuadXor1>(odd ? a0 : a1);
     const float lo = odd ? other : a0, hi = odd ? a1 : other;
     return (uint32_t)to_bits(lo, T{}) | ((uint32_t)to_bits(hi, T{}) << 16);
 }
@@ -162,10 +187,11 @@ struct DzEpilogue {
                 const int row = row0 + 16 * i + 4 * q4 + r;
                 const RowGrad w = __builtin_bit_cast(RowGrad, now[r]);
                 const int hot = w.label - v0 - col0 - c16;
+                const float shift = -w.lse * kLog2e;
                 float d[kNB];
 #pragma unroll
                 for (int j = 0; j < kNB; ++j) {
-                    const float p = __builtin_amdgcn_exp2f((acc_read(acc[i][j][r]) - w.lse) * kLog2e);
+                    const float p = __builtin_amdgcn_exp2f(fmaf(acc_read(acc[i][j][r]), kLog2e, shift));
                     d[j] = fmaf(w.g, p, hot == 16 * j ? -w.g : 0.0f);
                     if (EDGE && col0 + 16 * j + c16 >= N) d[j] = 0.0f;
                 }

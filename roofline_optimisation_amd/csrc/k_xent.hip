@@ -355,11 +355,14 @@ bool weights_load(unsigned flags, int N, int K, const void *W, int ldw) {
 // The time of M x N logits in one kind of tile, in rounds of 256 x 256 tiles (one per CU):
 // rounds of resident tiles times what a round takes, measured at K = 2048 (bf16, us: 256 x
 // 256 46, 128 x 256 33, 64 x 256 29 with one per CU and 60 with two, 64 x 128 12, 64 x 64 8
-// and 14).  Few rows are bound by reading W, for which many small tiles do best: 16 x 32000 x
+// and 14, 128 x 128 17 and 30).  Few rows are bound by reading W, for which many small tiles do best: 16 x 32000 x
 // 2048 51 / 41 / 38 / 26 / 26 us in this order, 256 x 8000 x 2048 48 / 36 / 32 / 17 / 21,
-// 256 x 32000 x 2048 54 / 43 / 44 / 52 / 59, 512 x 32000 x 1024 37 / 45 / 47.
+// 256 x 32000 x 2048 54 / 43 / 44 / 52 / 59, 512 x 32000 x 1024 37 / 45 / 47.  128 x 128 two
+// per CU has neither the largest tile's rate nor its last rows' waste: 276 x 104940 x 640 72
+// against 78 us in 128 x 256 and 92 in 256 x 256, 4096 x 32000 x 2048 474 against 392.
 double head_cost(int tile, int M, int N) {
-    constexpr double kOne[kHeadTiles] = {1.0, 0.72, 0.63, 0.27, 0.17}, kTwo[kHeadTiles] = {0, 0, 1.2, 0, 0.3};
+    constexpr double kOne[kHeadTiles] = {1.0, 0.72, 0.63, 0.27, 0.17, 0.36};
+    constexpr double kTwo[kHeadTiles] = {0, 0, 1.2, 0, 0.3, 0.6};
     const long tiles = (long)cdiv(M, kHeadRows[tile]) * cdiv(N, kHeadCols[tile]);
     if (kTwo[tile] > 0 && tiles > 256) return (double)((tiles + 511) / 512) * kTwo[tile];
     return (double)((tiles + 255) / 256) * kOne[tile];

@@ -25,13 +25,13 @@ struct HeadArgs {
 };
 
 // The tiles of a head's products, EM rows x EN columns.
-enum HeadTiles : int { kHead256 = 0, kHead128, kHead64, kHead64x128, kHead64x64, kHeadTiles };
-constexpr int kHeadRows[kHeadTiles] = {256, 128, 64, 64, 64};
-constexpr int kHeadCols[kHeadTiles] = {256, 256, 256, 128, 64};
+enum HeadTiles : int { kHead256 = 0, kHead128, kHead64, kHead64x128, kHead64x64, kHead128x128, kHeadTiles };
+constexpr int kHeadRows[kHeadTiles] = {256, 128, 64, 64, 64, 128};
+constexpr int kHeadCols[kHeadTiles] = {256, 256, 256, 128, 64, 128};
 // A trip of the tile's ring of loads; K is at least one.
-constexpr int kHeadTrip[kHeadTiles] = {128, 128, 128, 256, 256};
+constexpr int kHeadTrip[kHeadTiles] = {128, 128, 128, 256, 256, 128};
 // Columns of one wave, a block of the row statistics.
-constexpr int kStatCols[kHeadTiles] = {128, 128, 64, 64, 32};
+constexpr int kStatCols[kHeadTiles] = {128, 128, 64, 64, 32, 64};
 
 // Statistics of Z, W pointing at class v0, by blocks of kStatCols[tile] columns: part[block *
 // ldp + row] = (maximum, sum of exp(z - maximum)) and, where a row's label is one of these

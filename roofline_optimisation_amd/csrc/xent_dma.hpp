@@ -266,7 +266,7 @@ struct HeadTile {
     static constexpr int kEM = kHeadRows[TILE], kEN = kHeadCols[TILE];
     static constexpr int kWM = TILE == kHead64 ? 1 : 2, kWN = 4 / kWM;
     static constexpr int kNs = kHeadTrip[TILE] / dma::kBK;
-    static constexpr int kPerSimd = TILE == kHead64 || TILE == kHead64x64 ? 2 : 1;  // waves: workgroups per CU
+    static constexpr int kPerSimd = TILE == kHead64 || TILE == kHead64x64 || TILE == kHead128x128 ? 2 : 1;  // waves: workgroups per CU
     using G = dma::Geo<kEM, kEN, kWM, kWN, kNs, 0>;
     static_assert(kEN / kWN == kStatCols[TILE], "a statistics block is a wave's columns");
 };
@@ -346,7 +346,8 @@ hipError_t launch_head_layout(int tile, const HeadArgs &h, const EX &ex, hipStre
     case kHead128: return launch_head_tile<T, W_MN, kHead128>(h, ex, s);
     case kHead64: return launch_head_tile<T, W_MN, kHead64>(h, ex, s);
     case kHead64x128: return launch_head_tile<T, W_MN, kHead64x128>(h, ex, s);
-    default: return launch_head_tile<T, W_MN, kHead64x64>(h, ex, s);
+    case kHead64x64: return launch_head_tile<T, W_MN, kHead64x64>(h, ex, s);
+    default: return launch_head_tile<T, W_MN, kHead128x128>(h, ex, s);
     }
 }
 

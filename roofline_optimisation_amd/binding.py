@@ -10,7 +10,9 @@ Nothing here computes any part of the results: every step runs in the HIP kernel
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -213,6 +215,7 @@ def gemm355_row_sum_f32(rows, cols, X, ldx, out, stream=0) -> int:
     return lib().gemm355_row_sum_f32(rows, cols, X, ldx, out, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def gemm355_xent_workspace(dtype, flags, M, N, K) -> int:
     return lib().gemm355_xent_workspace(dtype, flags, M, N, K)
 
@@ -223,6 +226,7 @@ def gemm355_xent(dtype, flags, M, N, K, X, ldx, W, ldw, labels, ignore, loss, ls
                               workspace, workspace_bytes, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def gemm355_xent_grad_workspace(dtype, flags, M, N, K) -> int:
     return lib().gemm355_xent_grad_workspace(dtype, flags, M, N, K)
 
@@ -361,36 +365,31 @@ def row_sum(X, out=None, stream=None):
     return out
 
 
-class _on:
-    """A call on another stream than the current one, or on another device: that device and
-    stream are made the current ones around its allocations and launches (the memory it
-    allocates is then that stream's, and is not handed out again before the work on it is
-    done).  Without either, nothing is entered."""
+def _on(stream, device):
+    """(handle, context) of a call's stream.  A call on another stream than the current one,
+    or on another device, makes them the current ones around its allocations and launches
+    (the memory it allocates is then that stream's, and is not handed out again before the
+    work on it is done); else the context does nothing."""
+    import torch
+    index = device.index
+    handle = torch._C._cuda_getCurrentRawStream(index)
+    here = index == torch._C._cuda_getDevice()
+    if stream is None and here:
+        return handle, _NOTHING
+    contexts = contextlib.ExitStack()
+    if not here:
+        contexts.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        wanted = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if wanted != handle:
+            handle = wanted
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(handle, device=device)
+            contexts.enter_context(torch.cuda.stream(stream))
+    return handle, contexts
 
-    def __init__(self, stream, device):
-        import torch
-        cuda = torch.cuda
-        self.contexts = ()
-        index = device.index
-        self.handle = torch._C._cuda_getCurrentRawStream(index)
-        if index != cuda.current_device():
-            self.contexts = (cuda.device(device),)
-        if stream is not None:
-            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            if handle != self.handle:
-                self.handle = handle
-                if not hasattr(stream, "cuda_stream"):
-                    stream = cuda.ExternalStream(handle, device=device)
-                self.contexts += (cuda.stream(stream),)
 
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+_NOTHING = contextlib.nullcontext()
 
 
 _INT_MAX = 2 ** 31 - 1
@@ -420,26 +419,44 @@ def _row_stride(t, what) -> int:
 
 
 def _vector(t, what, dtype, n, device):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on {device}")
 
 
-def _head_shapes(X, W, labels, trans_b):
-    """(dtype code, flags, M, N, K) of a projection X.op(W) with labels."""
+@functools.lru_cache(maxsize=1)
+def _codes():
     import torch
-    if not (X.is_cuda and W.is_cuda) or X.device != W.device:
+    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+def _code(t) -> int:
+    code = _codes().get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported operand dtype {t.dtype}")
+    return code
+
+
+def _head_args(X, W, labels, trans_b, ignore_index):
+    """(dtype code, flags, M, N, K, X, ldx, W, ldw, labels) of a projection X.op(W) with
+    labels, the matrices and labels as addresses."""
+    import torch
+    device = X.device
+    if device.type != "cuda" or W.device != device:
         raise ValueError("X and W must be tensors on one CUDA device")
     if X.dtype != W.dtype:
         raise TypeError("X and W must have the same dtype")
     if X.dim() != 2 or W.dim() != 2:
         raise ValueError("expected 2-D tensors")
     M, K = X.shape
-    K2, N = (W.shape[1], W.shape[0]) if trans_b else tuple(W.shape)
+    N, K2 = W.shape if trans_b else W.shape[::-1]
     if K2 != K:
         raise ValueError("inner dimensions differ")
-    _vector(labels, "labels", torch.int64, M, X.device)
+    _vector(labels, "labels", torch.int64, M, device)
     _c_ints(M, N, K)
-    return _dtype_code(X), TRANS_B if trans_b else 0, M, N, K
+    if not -2 ** 63 <= ignore_index < 2 ** 63:
+        raise ValueError("ignore_index does not fit an int64")
+    return (_code(X), TRANS_B if trans_b else 0, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
+            _row_stride(W, "W"), labels.data_ptr())
 
 
 def linear_cross_entropy(X, W, labels, *, trans_b: bool = False, ignore_index: int = -100, stream=None):
@@ -449,15 +466,15 @@ def linear_cross_entropy(X, W, labels, *, trans_b: bool = False, ignore_index: i
     outside the vocabulary).  X is M x K, W is K x N, or N x K with trans_b (float32, float16
     or bfloat16, rows contiguous); labels int64.  Raises Gemm355Error on a non-OK status."""
     import torch
-    code, flags, M, N, K = _head_shapes(X, W, labels, trans_b)
-    if not -2 ** 63 <= ignore_index < 2 ** 63:
-        raise ValueError("ignore_index does not fit an int64")
-    with _on(stream, X.device) as handle:
-        loss, lse = X.new_empty(M, dtype=torch.float32), X.new_empty(M, dtype=torch.float32)
-        n = gemm355_xent_workspace(code, flags, M, N, K)
+    head = _head_args(X, W, labels, trans_b, ignore_index)
+    M = head[2]
+    n = gemm355_xent_workspace(*head[:5])
+    handle, context = _on(stream, X.device)
+    with context:
+        loss = X.new_empty(M, dtype=torch.float32)
+        lse = torch.empty_like(loss)
         ws = X.new_empty(n, dtype=torch.uint8)
-        st = gemm355_xent(code, flags, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
-                          _row_stride(W, "W"), labels.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, handle)
+        st = gemm355_xent(*head, ignore_index, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, handle)
     if st != OK:
         raise Gemm355Error(st, "gemm355_xent")
     return loss, lse
@@ -469,21 +486,19 @@ def linear_cross_entropy_grad(X, W, labels, lse, dloss, *, trans_b: bool = False
     through gemm355_xent_grad; lse as that call returned it, dloss float32 per row.  A
     gradient that is not needed is None.  Raises Gemm355Error on a non-OK status."""
     import torch
-    code, flags, M, N, K = _head_shapes(X, W, labels, trans_b)
-    if not -2 ** 63 <= ignore_index < 2 ** 63:
-        raise ValueError("ignore_index does not fit an int64")
+    head = _head_args(X, W, labels, trans_b, ignore_index)
+    M, K = head[2], head[4]
     _vector(lse, "lse", torch.float32, M, X.device)
     _vector(dloss, "dloss", torch.float32, M, X.device)
-    with _on(stream, X.device) as handle:
+    n = gemm355_xent_grad_workspace(*head[:5])
+    handle, context = _on(stream, X.device)
+    with context:
         dX = X.new_empty((M, K)) if need_dx else None
         dW = W.new_empty(W.shape) if need_dw else None
-        n = gemm355_xent_grad_workspace(code, flags, M, N, K)
         ws = X.new_empty(n, dtype=torch.uint8)
-        st = gemm355_xent_grad(code, flags, M, N, K, X.data_ptr(), _row_stride(X, "X"), W.data_ptr(),
-                               _row_stride(W, "W"), labels.data_ptr(), ignore_index, lse.data_ptr(), dloss.data_ptr(),
-                               dX.data_ptr() if need_dx else 0, max(K, 1),
-                               dW.data_ptr() if need_dw else 0, max(int(W.shape[1]), 1), ws.data_ptr(), n,
-                               handle)
+        st = gemm355_xent_grad(*head, ignore_index, lse.data_ptr(), dloss.data_ptr(),
+                               dX.data_ptr() if need_dx else 0, K or 1,
+                               dW.data_ptr() if need_dw else 0, W.shape[1] or 1, ws.data_ptr(), n, handle)
     if st != OK:
         raise Gemm355Error(st, "gemm355_xent_grad")
     return dX, dW
@@ -512,12 +527,13 @@ def route(logits, k: int, *, score: str = "softmax", bias=None, groups: int = 1,
     if not 1 <= k <= 64:
         raise ValueError("k must be from 1 to 64")
     _c_ints(rows, experts, groups, top_groups, group_top)
-    with _on(stream, logits.device) as handle:
+    handle, context = _on(stream, logits.device)
+    with context:
         ids = logits.new_empty((rows, k), dtype=torch.int32)
-        weights = logits.new_empty((rows, k), dtype=torch.float32)
+        weights = torch.empty_like(ids, dtype=torch.float32)
         counts = logits.new_empty(experts, dtype=torch.int32)
-        st = gemm355_route(_dtype_code(logits), flags, rows, experts, k, groups, top_groups, group_top,
-                           logits.data_ptr(), _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(), scale,
+        st = gemm355_route(_code(logits), flags, rows, experts, k, groups, top_groups, group_top, logits.data_ptr(),
+                           _row_stride(logits, "logits"), 0 if bias is None else bias.data_ptr(), scale,
                            ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), handle)
     if st != OK:
         raise Gemm355Error(st, "gemm355_route")
@@ -534,18 +550,17 @@ def route_grad(logits, ids, dweights, *, score: str = "softmax", renorm: bool = 
     if not logits.is_cuda or logits.dim() != 2:
         raise ValueError("logits must be a 2-D CUDA tensor")
     rows, experts = logits.shape
+    k = ids.shape[1] if ids.dim() == 2 else 0
     for t, what, dtype in ((ids, "ids", torch.int32), (dweights, "dweights", torch.float32)):
-        if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.device != logits.device \
-                or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous {dtype} tensor of {rows} rows on {logits.device}")
-    if ids.shape != dweights.shape:
-        raise ValueError("ids and dweights must have the same shape")
-    _c_ints(rows, experts, ids.shape[1])
-    with _on(stream, logits.device) as handle:
+        if t.dtype != dtype or t.shape != (rows, k) or t.device != logits.device or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor, rows x k, on {logits.device}")
+    _c_ints(rows, experts, k)
+    handle, context = _on(stream, logits.device)
+    with context:
         dx = logits.new_empty((rows, experts))
-        st = gemm355_route_grad(_dtype_code(logits), flags, rows, experts, int(ids.shape[1]), logits.data_ptr(),
-                                _row_stride(logits, "logits"), ids.data_ptr(), dweights.data_ptr(), scale, dx.data_ptr(),
-                                max(experts, 1), handle)
+        st = gemm355_route_grad(_code(logits), flags, rows, experts, k, logits.data_ptr(),
+                                _row_stride(logits, "logits"), ids.data_ptr(), dweights.data_ptr(), scale,
+                                dx.data_ptr(), experts or 1, handle)
     if st != OK:
         raise Gemm355Error(st, "gemm355_route_grad")
     return dx

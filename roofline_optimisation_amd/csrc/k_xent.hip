@@ -25,9 +25,6 @@ namespace {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kMaxDim = (1 << 30) - 1;
 
-// A row's running statistics: maximum m, sum l of exp(z - m), the label's logit.
-struct RowState { float m, l, z; };
-
 // (m, l) merged with another pair; an empty pair is (-infinity, 0).
 __device__ __forceinline__ void merge_pair(float &m, float &l, float mo, float lo) {
     const bool mine = m >= mo;
@@ -54,31 +51,35 @@ __device__ __forceinline__ void finish_row(int row, float m, float l, float z, i
                     : s - z;
 }
 
-// One workgroup per row of a piece Z (columns v0 .. v0 + nc of the logits): its statistics
-// merged into state[row] (or started, at v0 == 0); the last piece writes the results.
-__global__ __launch_bounds__(256) void xent_rows_kernel(int nc, int v0, int N, const float *__restrict__ Z,
-                                                        int ldz, const int64_t *__restrict__ labels,
-                                                        int64_t ignore, RowState *state, float *loss,
-                                                        float *lse) {
+constexpr int kChunk = 4096;  // columns of a row that one workgroup takes the statistics of
+
+// The statistics of columns [4096 b, + 4096) of row r of a piece Z, workgroup (b, r), to
+// part[b * ldp + r]; zl[r] = the label's logit where it is one of them (the piece starts at
+// class v0).
+__global__ __launch_bounds__(256) void xent_chunk_kernel(int nc, int v0, const float *__restrict__ Z, int ldz,
+                                                         const int64_t *__restrict__ labels, float2 *part, int ldp,
+                                                         float *zl) {
     __shared__ float sm[4], sl[4];
-    const int row = blockIdx.x, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int row = blockIdx.y, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int c0 = blockIdx.x * kChunk, c1 = min(c0 + kChunk, nc);
     const float *z = Z + (size_t)row * ldz;
     float m = kNegInf, l = 0.0f;
-    for (int base = 0; base < nc; base += 1024) {
-        float v[4], cm = kNegInf;
+    for (int base = c0; base < c1; base += 2048) {
+        float v[8], cm = kNegInf;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             const int c = base + 256 * u + (int)threadIdx.x;
-            v[u] = c < nc ? z[c] : kNegInf;
-            cm = fmaxf(cm, v[u]);
+            v[u] = c < c1 ? z[c] : kNegInf;
         }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) cm = fmaxf(cm, v[u]);
         if (cm > m) {
             l *= expf(m - cm);
             m = cm;
         }
         const float shift = m == kNegInf ? 0.0f : m;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) l += expf(v[u] - shift);
+        for (int u = 0; u < 8; ++u) l += expf(v[u] - shift);
     }
     wave_allreduce2(m, l, MergePair{});
     if (lane == 0) {
@@ -88,16 +89,12 @@ __global__ __launch_bounds__(256) void xent_rows_kernel(int nc, int v0, int N, c
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int w = 1; w < 4; ++w) merge_pair(m, l, sm[w], sl[w]);
-    RowState s{kNegInf, 0.0f, 0.0f};
-    if (v0 > 0) s = state[row];
-    merge_pair(s.m, s.l, m, l);
-    const int64_t label = labels[row];
-    if (label >= v0 && label < (int64_t)v0 + nc) s.z = z[label - v0];
-    if (v0 + nc < N) state[row] = s;
-    else finish_row(row, s.m, s.l, s.z, label, ignore, N, loss, lse);
+    part[(size_t)blockIdx.x * ldp + row] = make_float2(m, l);
+    const int64_t at = labels[row] - v0;
+    if (at >= c0 && at < c1) zl[row] = z[at];
 }
 
-// The statistics of the fused tiles: `blocks` pairs per row (part[block * ldp + row]) merged,
+// The statistics of the tiles or chunks: `blocks` pairs per row (part[block * ldp + row]) merged,
 // and the row's results written.  A workgroup takes R rows, 1024 / R threads a row: each
 // merges every (1024 / R)-th block, then the threads' pairs are merged in halves.
 template <int R>
@@ -252,6 +249,18 @@ __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *
     }
 }
 
+// out = the sum of n partial sums, `stride` apart.  Grid: (columns / 256, rows).
+__global__ __launch_bounds__(256) void xent_sum_kernel(int cols, const float *__restrict__ part, int n, size_t stride,
+                                                       float *out, int ldo) {
+    const int c = blockIdx.x * 256 + (int)threadIdx.x;
+    if (c >= cols) return;
+    const float *p = part + (size_t)blockIdx.y * cols + c;
+    float v = p[0];
+#pragma unroll 8
+    for (int i = 1; i < n; ++i) v += p[i * stride];
+    out[(size_t)blockIdx.y * ldo + c] = v;
+}
+
 template <typename E>
 __global__ void zero_matrix_kernel(int cols, E *out, int ld) {
     const int c = blockIdx.x * 256 + threadIdx.x;
@@ -296,22 +305,29 @@ int piece_cols(int M, int N) {
 constexpr int kRowBlock = 8192;  // rows whose logits are held at once in the forward pass
 
 struct ForwardPlan {
-    int rows, cols;
-    float *Z;
-    RowState *state;
+    int rows, cols, blocks, ldm;
+    float *Z, *zl;
+    float2 *part;
+    void *Xm;
     size_t bytes;
-    ForwardPlan(int M, int N, void *ws) {
+    ForwardPlan(int dtype, int M, int N, int K, void *ws) {
+        const size_t es = dtype == kF32 ? 4 : 2;
+        ldm = (int)up((size_t)(K > 0 ? K : 1), 16 / es);
         rows = M < kRowBlock ? M : kRowBlock;
         cols = piece_cols(rows, N);
+        blocks = 0;
+        for (int v0 = 0; v0 < N; v0 += cols) blocks += cdiv(N - v0 < cols ? N - v0 : cols, kChunk);
         Carver c{(char *)ws};
         Z = (float *)c.take((size_t)rows * cols * 4);
-        state = (RowState *)c.take((size_t)rows * sizeof(RowState));
+        part = (float2 *)c.take((size_t)blocks * rows * sizeof(float2));
+        zl = (float *)c.take((size_t)rows * 4);
+        Xm = c.take((size_t)rows * ldm * es);
         bytes = c.used;
     }
 };
 
 struct GradPlan {
-    int cols, ldm;
+    int cols, ldm, ranges, step;  // ranges of `step` classes dX is summed over; 0: one product
     float *scale, *Z, *dX, *dW;
     RowGrad *rows;
     void *Xm, *dZ;
@@ -321,13 +337,23 @@ struct GradPlan {
         const size_t es = h16 ? 2 : 4;
         cols = piece_cols(M, N);
         ldm = (int)up((size_t)(K > 0 ? K : 1), 16 / es);
+        ranges = step = 0;
+        // binary32 dX of fewer 64 x 64 tiles than CUs: four workgroups a CU, ranges of 256
+        // classes or more (16-bit types come here with fewer classes than that)
+        const long tiles = (long)cdiv(M, 64) * cdiv(K > 0 ? K : 1, 64);
+        const int nc = cols < N ? cols : N;
+        if (!h16 && tiles < 256 && nc >= 512) {
+            const int want = (int)(1024 / tiles);
+            step = (int)up((size_t)std::max(cdiv(nc, want), 256), 32);
+            ranges = cdiv(nc, step);
+        }
         Carver c{(char *)ws};
         scale = (float *)c.take(8);
         rows = (RowGrad *)c.take((size_t)M * sizeof(RowGrad));
         Xm = c.take((size_t)M * ldm * es);
         Z = (float *)c.take((size_t)M * cols * 4);
         dZ = h16 ? c.take((size_t)M * cols * 2) : Z;
-        dX = h16 ? (float *)c.take((size_t)M * K * 4) : nullptr;
+        dX = h16 || ranges > 0 ? (float *)c.take((size_t)std::max(ranges, 1) * M * K * 4) : nullptr;
         dW = h16 ? (float *)c.take((size_t)cols * K * 4) : nullptr;
         bytes = c.used;
     }
@@ -536,14 +562,14 @@ gemm355_status status_of(hipError_t e) { return e == hipSuccess ? GEMM355_OK : G
         if (try_e != hipSuccess) return GEMM355_ERR_LAUNCH; \
     } while (0)
 
-hipError_t merge(int M, int N, int blocks, const FusedForwardPlan &p, const int64_t *labels, int64_t ignore, float *loss,
-                 float *lse, hipStream_t s) {
+hipError_t merge(int M, int N, int blocks, const float2 *part, int ldp, const float *zl, const int64_t *labels,
+                 int64_t ignore, float *loss, float *lse, hipStream_t s) {
     if (M >= 32)
-        hipLaunchKernelGGL((xent_merge_kernel<32>), dim3(cdiv(M, 32)), dim3(1024), 0, s, M, N, blocks, p.part,
-                           p.rows, p.zl, labels, ignore, loss, lse);
+        hipLaunchKernelGGL((xent_merge_kernel<32>), dim3(cdiv(M, 32)), dim3(1024), 0, s, M, N, blocks, part, ldp, zl,
+                           labels, ignore, loss, lse);
     else
-        hipLaunchKernelGGL((xent_merge_kernel<4>), dim3(cdiv(M, 4)), dim3(1024), 0, s, M, N, blocks, p.part,
-                           p.rows, p.zl, labels, ignore, loss, lse);
+        hipLaunchKernelGGL((xent_merge_kernel<4>), dim3(cdiv(M, 4)), dim3(1024), 0, s, M, N, blocks, part, ldp, zl,
+                           labels, ignore, loss, lse);
     return hipGetLastError();
 }
 
@@ -593,8 +619,8 @@ gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, con
                 blocks += stat_blocks(c);
             }
         }
-        G355_TRY(merge(rows, N, blocks, p, labels + r0, ignore, loss ? loss + r0 : nullptr, lse ? lse + r0 : nullptr,
-                       s));
+        G355_TRY(merge(rows, N, blocks, p.part, p.rows, p.zl, labels + r0, ignore, loss ? loss + r0 : nullptr,
+                       lse ? lse + r0 : nullptr, s));
     }
     return GEMM355_OK;
 }
@@ -602,21 +628,30 @@ gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, con
 gemm355_status forward(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
                        int ldw, const int64_t *labels, int64_t ignore, float *loss, float *lse, void *ws,
                        hipStream_t s) {
-    const ForwardPlan p(M, N, ws);
+    const ForwardPlan p(dtype, M, N, K, ws);
     const size_t es = dtype == kF32 ? 4 : 2;
+    // rows of X that are not 16-byte aligned are copied: the copy is M x K, and every tile of
+    // the product would load its rows element by element
+    const bool copy_x = !rows_aligned16(X, ldx, (int)es);
     for (int r0 = 0; r0 < M; r0 += p.rows) {
         const int rows = M - r0 < p.rows ? M - r0 : p.rows;
+        const void *x = at(X, (size_t)r0 * ldx, es);
+        const int u = (int)es / 2;   // 16-bit units an element
+        if (copy_x) G355_TRY(copy_rows(rows, rows, K * u, x, ldx * u, (uint16_t *)p.Xm, p.ldm * u, s));
+        int blocks = 0;
         for (int v0 = 0; v0 < N; v0 += p.cols) {
             const int nc = N - v0 < p.cols ? N - v0 : p.cols;
             const gemm355_status st =
-                gemm355_gemm_ex(GEMM355_VARIANT_AUTO, dtype, flags, rows, nc, K, at(X, (size_t)r0 * ldx, es), ldx,
-                                at(W, w_offset(flags, v0, ldw), es), ldw, p.Z, p.cols, s);
+                gemm355_gemm_ex(GEMM355_VARIANT_AUTO, dtype, flags, rows, nc, K, copy_x ? p.Xm : x,
+                                copy_x ? p.ldm : ldx, at(W, w_offset(flags, v0, ldw), es), ldw, p.Z, p.cols, s);
             if (st != GEMM355_OK) return st;
-            hipLaunchKernelGGL(xent_rows_kernel, dim3(rows), dim3(256), 0, s, nc, v0, N, p.Z, p.cols,
-                               labels + r0, ignore, p.state, loss ? loss + r0 : nullptr, lse ? lse + r0 : nullptr);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return status_of(e);
+            hipLaunchKernelGGL(xent_chunk_kernel, dim3(cdiv(nc, kChunk), rows), dim3(256), 0, s, nc, v0, p.Z, p.cols,
+                               labels + r0, p.part + (size_t)blocks * p.rows, p.rows, p.zl);
+            G355_TRY(hipGetLastError());
+            blocks += cdiv(nc, kChunk);
         }
+        G355_TRY(merge(rows, N, blocks, p.part, p.rows, p.zl, labels + r0, ignore, loss ? loss + r0 : nullptr,
+                       lse ? lse + r0 : nullptr, s));
     }
     return GEMM355_OK;
 }
@@ -780,7 +815,10 @@ gemm355_status gradient(const GradCall &a, void *ws) {
         if (st != GEMM355_OK) return st;
         e = piece_dz(a, p, v0, nc);
         if (e != hipSuccess) return status_of(e);
-        if (a.dX != nullptr) {
+        if (a.dX != nullptr && p.ranges > 0) {
+            const F32SplitArgs q{a.M, a.K, nc, p.Z, p.cols, (const float *)w, a.ldw, p.dX, p.step, v0 > 0};
+            G355_TRY(launch_xent_dx_f32(tb, q, a.s));
+        } else if (a.dX != nullptr) {
             st = gemm355_gemm_ex(GEMM355_VARIANT_AUTO, a.dtype,
                                  (tb ? 0u : (unsigned)GEMM355_TRANS_B) | (v0 > 0 ? (unsigned)GEMM355_ACCUMULATE : 0u),
                                  a.M, a.K, nc, p.dZ, p.cols, w, a.ldw, dx, lddx, a.s);
@@ -803,6 +841,11 @@ gemm355_status gradient(const GradCall &a, void *ws) {
             }
         }
     }
+    if (p.ranges > 0 && a.dX != nullptr)
+        return status_of(over_rows(a.M, [&](int r, int n) {
+            hipLaunchKernelGGL(xent_sum_kernel, dim3(cdiv(a.K, 256), n), dim3(256), 0, a.s, a.K, p.dX + (size_t)r * a.K,
+                               p.ranges, (size_t)a.M * a.K, (float *)a.dX + (size_t)r * a.lddx, a.lddx);
+        }));
     if (h16 && a.dX != nullptr) return status_of(round16(a, a.M, a.K, p.dX, a.K, 1, 0, p.scale, a.dX, a.lddx));
     return GEMM355_OK;
 }
@@ -817,7 +860,7 @@ extern "C" {
 
 size_t gemm355_xent_workspace(int dtype, unsigned flags, int M, int N, int K) {
     if (!valid_shape(dtype, flags, M, N, K) || M == 0) return 0;
-    const size_t any = ForwardPlan(M, N, nullptr).bytes;
+    const size_t any = ForwardPlan(dtype, M, N, K, nullptr).bytes;
     if (!fused_shape(dtype, N, K)) return any;
     // which one runs depends on W's alignment
     return std::max({any, FusedForwardPlan(false, flags, M, N, K, nullptr).bytes,

@@ -79,4 +79,18 @@ hipError_t launch_xent_dx_bf16(int tile, bool b_mn, const ProductArgs &p, hipStr
 hipError_t launch_xent_dw_f16(int tile, const ProductArgs &p, hipStream_t s);
 hipError_t launch_xent_dw_bf16(int tile, const ProductArgs &p, hipStream_t s);
 
+// dX's product in binary32 over ranges of `step` classes (a multiple of 32): range r's sums,
+// M x K, at part + r M K, added to what is there when `add`.  dZ (M x nc, row stride ldz) has
+// rows on 16-byte boundaries; W as in HeadArgs, without its conditions.
+struct F32SplitArgs {
+    int M, K, nc;
+    const float *dZ;
+    int ldz;
+    const float *W;
+    int ldw;
+    float *part;
+    int step, add;
+};
+hipError_t launch_xent_dx_f32(bool trans_b, const F32SplitArgs &p, hipStream_t s);
+
 }  // namespace g355

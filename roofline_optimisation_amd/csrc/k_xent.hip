@@ -151,9 +151,10 @@ __global__ __launch_bounds__(256) void xent_copy_kernel(int rows, int cols, cons
 // 2^100), the rows' RowGrad, and Xm = X with the rows without a label set to zero (their
 // products with a zero row of dZ would not be zero where X holds an infinity or NaN).
 // Every workgroup finds the same maximum over all rows, then does its share of the rows.
-// Rows from M to Mp are rows without a label.
+// Rows from M to Mp are rows without a label; with `again`, rows from `again` on are the
+// first ones' X again.
 template <typename E>
-__global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int N, int K, const E *__restrict__ X, int ldx,
+__global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int again, int N, int K, const E *__restrict__ X, int ldx,
                                                         const int64_t *__restrict__ labels, int64_t ignore,
                                                         const float *__restrict__ lse,
                                                         const float *__restrict__ dloss, int rescale,
@@ -178,11 +179,12 @@ __global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int N, in
         scale[1] = 1.0f / S;
     }
     for (int r = blockIdx.x; r < Mp; r += gridDim.x) {
-        const int64_t y = r < M ? labels[r] : -1;
-        const bool live = r < M && y != ignore && y >= 0 && y < N;
+        const int from = again > 0 && r >= again ? r - again : r;
+        const int64_t y = from < M ? labels[from] : -1;
+        const bool live = from < M && y != ignore && y >= 0 && y < N;
         if (threadIdx.x == 0)
-            rows[r] = RowGrad{live ? lse[r] : 0.0f, live ? dloss[r] * S : 0.0f, live ? (int)y : -1, 0};
-        const E *x = X + (size_t)r * ldx;
+            rows[r] = RowGrad{live ? lse[from] : 0.0f, live ? dloss[from] * S : 0.0f, live ? (int)y : -1, 0};
+        const E *x = X + (size_t)from * ldx;
         E *o = Xm + (size_t)r * ldm;
         if (vec) {   // rows of X and Xm 16-byte aligned, K a whole number of 16-byte chunks
             constexpr int kV = 16 / sizeof(E);
@@ -215,11 +217,11 @@ __global__ __launch_bounds__(256) void xent_dz_kernel(int nc, int v0, const floa
     }
 }
 
-// out = scale[1] * (the sum of `splits` partial sums, `stride` apart), rounded to the 16-bit
-// type; four columns per thread (VEC: in one access each).  Grid: (columns / 1024, rows).
+// out = scale[1] * (the sum of `splits` partial sums, `stride` apart, and with `other` of those
+// that many elements further on), rounded to the 16-bit type; four columns per thread (VEC: in one access each).  Grid: (columns / 1024, rows).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *__restrict__ acc, int lda,
-                                                         int splits, size_t stride,
+                                                         int splits, size_t stride, size_t other,
                                                          const float *__restrict__ scale, uint16_t *out,
                                                          int ldo) {
     const int c = blockIdx.x * 1024 + 4 * (int)threadIdx.x;
@@ -238,12 +240,23 @@ __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *
             for (int u = 0; u < 4; ++u) v += w[u];
         }
         for (; i < splits; ++i) v += *(const floatx4 *)(a + i * stride);
+        if (other > 0) {
+            floatx4 w = *(const floatx4 *)(a + other);   // the remainders' sums, small ones
+#pragma unroll 4
+            for (int k = 1; k < splits; ++k) w += *(const floatx4 *)(a + other + k * stride);
+            v += w;
+        }
         *(uint2 *)o = make_uint2((uint32_t)to_bits(f * v[0], T{}) | (uint32_t)to_bits(f * v[1], T{}) << 16,
                                  (uint32_t)to_bits(f * v[2], T{}) | (uint32_t)to_bits(f * v[3], T{}) << 16);
     } else {
         for (int u = 0; u < 4 && c + u < cols; ++u) {
             float v = a[u];
             for (int i = 1; i < splits; ++i) v += a[i * stride + u];
+            if (other > 0) {
+                float w = a[other + u];
+                for (int i = 1; i < splits; ++i) w += a[other + i * stride + u];
+                v += w;
+            }
             o[u] = to_bits(f * v, T{});
         }
     }
@@ -425,7 +438,7 @@ int head_sections(int M, int N, int K, Section out[2]) {
 // with the number of ranges that fill the CUs, so fewer rows take smaller tiles (M = 512, K
 // = 1024 in 16 ranges of 128 x 256 tiles against 32 of 256 x 256: 80 against 86 us with the
 // dZ before it; 1024 x 2048 the same, 2047 x 2048 479 against 436).
-int dx_tile(int M) { return M <= 64 ? kHead64 : M <= 512 ? kHead128 : kHead256; }
+int dx_tile(int M) { return M <= 512 ? kHead128 : kHead256; }
 
 // dW's product, `across` tiles of 256 over the hidden size: 128 x 128 tiles two per CU where
 // the sum over the rows is short and the stores of one tile hide behind the other's sum (512
@@ -502,8 +515,16 @@ struct Splits {
 
 constexpr long kDzBytes = 1L << 29;  // dZ of a piece
 
+// Up to this many rows dZ is kept in two parts, the rounded values in rows [0, 64) and what
+// the rounding leaves in rows [64, 128), which the products read as rows of their own (X's
+// again): dW's needs 128 rows of a ring trip in any case, and with few rows all the products
+// are bound by reading W and writing dW.  dX and dW are then off by little more than their own
+// rounding, where one part adds as much again.
+constexpr int kFewRows = 64;
+
 struct FusedGradPlan {
-    int cols, Mp, Kp, ldw, dx, splits, ldx;
+    bool few;
+    int cols, Mp, Kp, ldw, dx, dx_rows, splits, ldx;
     float *scale, *dX;
     RowGrad *rows;
     uint16_t *Xm, *dZ, *Wm;
@@ -511,16 +532,18 @@ struct FusedGradPlan {
     FusedGradPlan(bool copied, unsigned flags, int M, int N, int K, void *ws) {
         Mp = (int)up((size_t)M, 128);  // whole ring trips of dW's product, zeros past M
         Kp = padded_hidden(K);
-        dx = dx_tile(M);
+        few = M <= kFewRows;
+        dx_rows = few ? 2 * kFewRows : M;
+        dx = dx_tile(dx_rows);
         long fit = kDzBytes / 2 / Mp;
         if (copied && kCopyBytes / 2 / Kp < fit) fit = kCopyBytes / 2 / Kp;
         cols = even_pieces(N, fit);
         ldw = flags & GEMM355_TRANS_B ? Kp : cols;
         // dX's product: as many ranges of a piece's classes as fill the 256 CUs
         const int nc = cols < N ? cols : N;
-        splits = Splits(nc, 256 / (cdiv(M, kHeadRows[dx]) * cdiv(K, kHeadCols[dx]))).count;
+        splits = Splits(nc, 256 / (cdiv(dx_rows, kHeadRows[dx]) * cdiv(K, kHeadCols[dx]))).count;
         ldx = (int)up((size_t)K, 4);
-        dx_stride = (size_t)M * ldx;
+        dx_stride = (size_t)dx_rows * ldx;
         Carver c{(char *)ws};
         scale = (float *)c.take(8);
         rows = (RowGrad *)c.take((size_t)Mp * sizeof(RowGrad));
@@ -674,15 +697,15 @@ struct GradCall {
     hipStream_t s;
 };
 
-hipError_t prep(const GradCall &a, int Mp, float *scale, RowGrad *rows, void *Xm, int ldm) {
+hipError_t prep(const GradCall &a, int Mp, int again, float *scale, RowGrad *rows, void *Xm, int ldm) {
     const dim3 grid(Mp < 1024 ? Mp : 1024);
     const size_t es = a.dtype == kF32 ? 4 : 2;
     const int vec = rows_aligned16(a.X, a.ldx, (int)es) && a.K % (16 / es) == 0;
     if (a.dtype == kF32)
-        hipLaunchKernelGGL((xent_prep_kernel<float>), grid, dim3(256), 0, a.s, a.M, Mp, a.N, a.K, (const float *)a.X,
+        hipLaunchKernelGGL((xent_prep_kernel<float>), grid, dim3(256), 0, a.s, a.M, Mp, again, a.N, a.K, (const float *)a.X,
                            a.ldx, a.labels, a.ignore, a.lse, a.dloss, 0, scale, rows, (float *)Xm, ldm, vec);
     else
-        hipLaunchKernelGGL((xent_prep_kernel<uint16_t>), grid, dim3(256), 0, a.s, a.M, Mp, a.N, a.K,
+        hipLaunchKernelGGL((xent_prep_kernel<uint16_t>), grid, dim3(256), 0, a.s, a.M, Mp, again, a.N, a.K,
                            (const uint16_t *)a.X, a.ldx, a.labels, a.ignore, a.lse, a.dloss,
                            a.dtype == kF16 ? 1 : 0, scale, rows, (uint16_t *)Xm, ldm, vec);
     return hipGetLastError();
@@ -705,12 +728,12 @@ hipError_t piece_dz(const GradCall &a, const GradPlan &p, int v0, int nc) {
 }
 
 hipError_t round16(const GradCall &a, int rows, int cols, const float *acc, int lda, int splits, size_t stride,
-                   const float *scale, void *out, int ldo) {
-    const bool vec = cols % 4 == 0 && lda % 4 == 0 && stride % 4 == 0 && ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
+                   size_t other, const float *scale, void *out, int ldo) {
+    const bool vec = cols % 4 == 0 && lda % 4 == 0 && stride % 4 == 0 && other % 4 == 0 && ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
     return over_rows(rows, [&](int r, int n) {
         const auto go = [&](auto t, auto v) {
             hipLaunchKernelGGL((xent_round_kernel<decltype(t), decltype(v)::value>), dim3(cdiv(cols, 1024), n),
-                               dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda, splits, stride, scale,
+                               dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda, splits, stride, other, scale,
                                (uint16_t *)out + (size_t)r * ldo, ldo);
         };
         const auto typed = [&](auto t) { vec ? go(t, std::true_type{}) : go(t, std::false_type{}); };
@@ -722,8 +745,8 @@ hipError_t round16(const GradCall &a, int rows, int cols, const float *acc, int 
 gemm355_status gradient_fused(const GradCall &a, bool copied, void *ws) {
     const FusedGradPlan p(copied, a.flags, a.M, a.N, a.K, ws);
     const bool tb = a.flags & GEMM355_TRANS_B, f16 = a.dtype == kF16;
-    G355_TRY(prep(a, p.Mp, p.scale, p.rows, p.Xm, p.Kp));
-    const bool one = p.cols >= a.N && p.splits == 1;  // dX in one product
+    G355_TRY(prep(a, p.Mp, p.few ? kFewRows : 0, p.scale, p.rows, p.Xm, p.Kp));
+    const bool one = !p.few && p.cols >= a.N && p.splits == 1;  // dX in one product
     for (int v0 = 0; v0 < a.N; v0 += p.cols) {
         const int nc = a.N - v0 < p.cols ? a.N - v0 : p.cols;
         const auto *w = (const uint16_t *)at(a.W, w_offset(a.flags, v0, a.ldw), 2);
@@ -731,18 +754,19 @@ gemm355_status gradient_fused(const GradCall &a, bool copied, void *ws) {
         if (copied) w = p.Wm;
         const int lw = copied ? p.ldw : a.ldw;
         Section part[2];
-        const int dz_parts = head_sections(p.Mp, nc, p.Kp, part);
+        const int dz_rows = p.few ? kFewRows : p.Mp;
+        const int dz_parts = head_sections(dz_rows, nc, p.Kp, part);
         for (int i = 0; i < dz_parts; ++i) {
             const Section &c = part[i];
-            const HeadArgs h{p.Mp, c.cols, p.Kp, p.Xm, p.Kp, w + w_offset(a.flags, c.v0, lw), lw, tb};
-            uint16_t *dZ = p.dZ + c.v0;
-            G355_TRY(f16 ? launch_xent_dz_f16(c.tile, h, p.rows, v0 + c.v0, dZ, p.cols, a.s)
-                         : launch_xent_dz_bf16(c.tile, h, p.rows, v0 + c.v0, dZ, p.cols, a.s));
+            const HeadArgs h{dz_rows, c.cols, p.Kp, p.Xm, p.Kp, w + w_offset(a.flags, c.v0, lw), lw, tb};
+            uint16_t *dZ = p.dZ + c.v0, *lo = p.few ? dZ + (size_t)kFewRows * p.cols : nullptr;
+            G355_TRY(f16 ? launch_xent_dz_f16(c.tile, h, p.rows, v0 + c.v0, dZ, lo, p.cols, a.s)
+                         : launch_xent_dz_bf16(c.tile, h, p.rows, v0 + c.v0, dZ, lo, p.cols, a.s));
         }
         if (a.dX != nullptr) {
             const Splits sp(nc, p.splits);
             ProductArgs q{};
-            q.M = q.rows = a.M;
+            q.M = q.rows = p.dx_rows;
             q.N = p.Kp;
             q.cols = a.K;
             q.K = nc;
@@ -786,7 +810,8 @@ gemm355_status gradient_fused(const GradCall &a, bool copied, void *ws) {
         }
     }
     if (!one && a.dX != nullptr)
-        G355_TRY(round16(a, a.M, a.K, p.dX, p.ldx, p.splits, p.dx_stride, p.scale, a.dX, a.lddx));
+        G355_TRY(round16(a, a.M, a.K, p.dX, p.ldx, p.splits, p.dx_stride, p.few ? (size_t)kFewRows * p.ldx : 0, p.scale,
+                         a.dX, a.lddx));
     return GEMM355_OK;
 }
 
@@ -803,7 +828,7 @@ gemm355_status gradient(const GradCall &a, void *ws) {
     const GradPlan p(a.dtype, a.M, a.N, a.K, ws);
     const bool h16 = a.dtype != kF32, tb = a.flags & GEMM355_TRANS_B;
     const size_t es = h16 ? 2 : 4;
-    hipError_t e = prep(a, a.M, p.scale, p.rows, p.Xm, p.ldm);
+    hipError_t e = prep(a, a.M, 0, p.scale, p.rows, p.Xm, p.ldm);
     if (e != hipSuccess) return status_of(e);
     float *dx = h16 ? p.dX : (float *)a.dX;
     const int lddx = h16 ? a.K : a.lddx;
@@ -836,7 +861,7 @@ gemm355_status gradient(const GradCall &a, void *ws) {
                                       p.dZ, p.cols, out, ldo, a.s);
             if (st != GEMM355_OK) return st;
             if (h16) {
-                e = round16(a, rows, cols, out, ldo, 1, 0, p.scale, dw, a.lddw);
+                e = round16(a, rows, cols, out, ldo, 1, 0, 0, p.scale, dw, a.lddw);
                 if (e != hipSuccess) return status_of(e);
             }
         }
@@ -846,7 +871,7 @@ gemm355_status gradient(const GradCall &a, void *ws) {
             hipLaunchKernelGGL(xent_sum_kernel, dim3(cdiv(a.K, 256), n), dim3(256), 0, a.s, a.K, p.dX + (size_t)r * a.K,
                                p.ranges, (size_t)a.M * a.K, (float *)a.dX + (size_t)r * a.lddx, a.lddx);
         }));
-    if (h16 && a.dX != nullptr) return status_of(round16(a, a.M, a.K, p.dX, a.K, 1, 0, p.scale, a.dX, a.lddx));
+    if (h16 && a.dX != nullptr) return status_of(round16(a, a.M, a.K, p.dX, a.K, 1, 0, 0, p.scale, a.dX, a.lddx));
     return GEMM355_OK;
 }
 

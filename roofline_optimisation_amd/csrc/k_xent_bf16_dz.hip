@@ -3,9 +3,9 @@
 
 namespace g355 {
 
-hipError_t launch_xent_dz_bf16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
-                              hipStream_t s) {
-    return launch_head<bf16_t>(tile, h, DzEpilogue<bf16_t>{h.M, h.N, v0, rows, dZ, ldz}, s);
+hipError_t launch_xent_dz_bf16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, uint16_t *lo,
+                              int ldz, hipStream_t s) {
+    return launch_head<bf16_t>(tile, h, DzEpilogue<bf16_t>{h.M, h.N, v0, rows, dZ, lo, ldz}, s);
 }
 
 }  // namespace g355

@@ -42,11 +42,12 @@ hipError_t launch_xent_stats_bf16(int tile, const HeadArgs &h, const int64_t *la
                                   int ldp, float *zl, hipStream_t s);
 
 // dZ (M x N rounded up to a multiple of 8, row stride ldz, the added columns 0) of the
-// classes v0 .. v0 + N, W pointing at the first of them.
-hipError_t launch_xent_dz_f16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
-                              hipStream_t s);
-hipError_t launch_xent_dz_bf16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, int ldz,
-                               hipStream_t s);
+// classes v0 .. v0 + N, W pointing at the first of them.  lo, if not NULL, takes what the
+// rounding of dZ leaves over, rounded in turn.
+hipError_t launch_xent_dz_f16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, uint16_t *lo,
+                              int ldz, hipStream_t s);
+hipError_t launch_xent_dz_bf16(int tile, const HeadArgs &h, const RowGrad *rows, int v0, uint16_t *dZ, uint16_t *lo,
+                               int ldz, hipStream_t s);
 
 // A product of the gradient: op(A).op(B) over K.  A is M x K (k-contiguous), or K x M with
 // a_mn; B is N x K, or K x N with b_mn.  M and N bound the loads (multiples of 8 where the
@@ -71,7 +72,7 @@ struct ProductArgs {
 
 // dX's product: A = dZ (k-contiguous), B m/n-contiguous or not; partial sums, or the 16-bit
 // result when p.part is NULL.  Tiles
-// kHead256, kHead128 and kHead64.
+// kHead256 and kHead128.
 hipError_t launch_xent_dx_f16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s);
 hipError_t launch_xent_dx_bf16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s);
 // dW's product: both operands m/n-contiguous, K a multiple of 128, 16-bit result.  Square

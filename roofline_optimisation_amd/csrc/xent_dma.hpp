@@ -110,9 +110,9 @@ struct StatsEpilogue {
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    m[r] = x[r][0];
+                    m[r] = x[r][0];   // three-operand maxima: fewer instructions than max2's
 #pragma unroll
-                    for (int j = 1; j < kNB; ++j) m[r] = max2(m[r], x[r][j]);
+                    for (int j = 1; j < kNB; ++j) m[r] = fmaxf(m[r], x[r][j]);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) m[r] = row16_max(m[r]);
@@ -151,12 +151,12 @@ __device__ __forceinline__ uint32_t pair_word(float a0, float a1, int odd) {
 }
 
 // dZ of the wave's tile: g (exp(z - lse) - [column is the label]), rounded to T.  Columns
-// from N to the next multiple of 8 are written as 0.
+// from N to the next multiple of 8 are written as 0.  lo: the rounding's remainders, too.
 template <typename T>
 struct DzEpilogue {
     int M, N, v0;
     const RowGrad *rg;
-    uint16_t *out;
+    uint16_t *out, *lo;
     int ldo;
     __device__ int rows() const { return M; }
     __device__ int cols() const { return N; }
@@ -195,11 +195,19 @@ struct DzEpilogue {
                     d[j] = fmaf(w.g, p, hot == 16 * j ? -w.g : 0.0f);
                     if (EDGE && col0 + 16 * j + c16 >= N) d[j] = 0.0f;
                 }
-                uint16_t *o = out + (size_t)row * ldo + cw;
+                const size_t at = (size_t)row * ldo + cw;
 #pragma unroll
                 for (int j = 0; j < kNB; j += 2) {
                     const uint32_t v = pair_word<T>(d[j], d[j + 1], odd);
-                    if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(o + 16 * j) = v;
+                    if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(out + at + 16 * j) = v;
+                }
+                if (lo != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < kNB; j += 2) {
+                        const uint32_t v = pair_word<T>(d[j] - to_float(T{to_bits(d[j], T{})}),
+                                                        d[j + 1] - to_float(T{to_bits(d[j + 1], T{})}), odd);
+                        if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(lo + at + 16 * j) = v;
+                    }
                 }
             }
         }
@@ -374,8 +382,6 @@ template <typename T, bool B_MN>
 hipError_t launch_dx_layout(int tile, const ProductArgs &p, hipStream_t s) {
     // the ranges before the last are whole ring trips
     const bool kr = p.K % 128 != 0;
-    if (tile == kHead64)
-        return kr ? launch_dx_epi<T, B_MN, kHead64, true>(p, s) : launch_dx_epi<T, B_MN, kHead64, false>(p, s);
     if (tile == kHead128)
         return kr ? launch_dx_epi<T, B_MN, kHead128, true>(p, s) : launch_dx_epi<T, B_MN, kHead128, false>(p, s);
     return kr ? launch_dx_epi<T, B_MN, kHead256, true>(p, s) : launch_dx_epi<T, B_MN, kHead256, false>(p, s);

@@ -69,7 +69,7 @@ def xent(X, W, labels, dtype, ignore=-100):
     return loss, lse, ltol, tol
 
 
-def xent_grad(X, W, labels, lse, dloss, dtype, ignore=-100):
+def xent_grad(X, W, labels, lse, dloss, dtype, ignore=-100, parts=1):
     """(dX, dW as N x K, bound of dX, bound of dW) in binary64, for the given lse.
 
     dZ = g (p - onehot), p = exp(Z - lse).  An error d of the argument moves p by p d: d is
@@ -92,7 +92,8 @@ def xent_grad(X, W, labels, lse, dloss, dtype, ignore=-100):
     p = np.exp(Z - lse[:, None])
     dz = g[:, None] * (p - hot)
     moved = np.expm1(e + U24 * (4 * np.abs(lse[:, None]) + 2 * np.abs(Z) + 16))
-    half = HALF[dtype] if dtype != "f32" else 0.0
+    # rounded in two parts, the second is off by half a step of what the first leaves
+    half = HALF[dtype] ** parts if dtype != "f32" else 0.0
     err = np.abs(g)[:, None] * p * moved + 3 * U24 * np.abs(dz)
     err += half * (np.abs(dz) + err)
     if dtype == "f16" and np.abs(g).max() > 0:

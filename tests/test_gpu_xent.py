@@ -114,9 +114,9 @@ def run_grad(h, lse, dloss, need=(True, True), padx=0, padw=0, ignore=-100):
     return got
 
 
-def check_grad(h, lse, dloss, what, ignore=-100, **kw):
+def check_grad(h, lse, dloss, what, ignore=-100, parts=1, **kw):
     dX, dW = run_grad(h, lse, dloss, ignore=ignore, **kw)
-    wX, wW, tX, tW = ref.xent_grad(h.X, h.W, h.labels, lse, dloss, h.dtype, ignore)
+    wX, wW, tX, tW = ref.xent_grad(h.X, h.W, h.labels, lse, dloss, h.dtype, ignore, parts)
     for name, got, want, tol in (("dX", dX, wX, tX), ("dW", dW, wW, tW)):
         if got is None:
             continue
@@ -233,6 +233,17 @@ def test_binary16_upstream_of_any_size(exponent):
     h = Head(X, W, y, "f16", True)
     lse = ref.xent(X, W, y, "f16")[1].astype(np.float32)
     check_grad(h, lse, upstream(80, 6, "f32") * np.float32(2.0 ** exponent), exponent)
+
+
+@pytest.mark.parametrize("trans_b", [True, False])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 128), (7, 2600, 256), (33, 1003, 136), (64, 5000, 520), (64, 256, 100)])
+def test_few_rows_keep_two_parts(M, N, K, dtype, trans_b):
+    """Up to 64 rows the rounding of dZ adds next to nothing to the results' own."""
+    X, W, y = ref.make_head(M, N, K, dtype, 15 + M, ignored=M > 1)
+    h = Head(X, W, y, dtype, trans_b)
+    lse = ref.xent(X, W, y, dtype)[1].astype(np.float32)
+    check_grad(h, lse, upstream(M, 8, dtype), (M, N, K), parts=2)
 
 
 def test_zero_upstream():

@@ -522,10 +522,18 @@ constexpr long kDzBytes = 1L << 29;  // dZ of a piece
 // rounding, where one part adds as much again.
 constexpr int kFewRows = 64;
 
+// Ranges of the rows that dW's product is summed over, 1 for none: with few 128 x 128 tiles
+// and many rows, as many as fill the CUs twice (6948 rows, 1175 classes, K = 576: 50 tiles of
+// 55 trips each on as many CUs).
+int dw_splits(int Mp, int nc, int K) {
+    const long tiles = (long)cdiv(nc, 128) * cdiv(K, 128);
+    return tiles < 256 ? Splits(Mp, (int)(512 / tiles)).count : 1;
+}
+
 struct FusedGradPlan {
     bool few;
     int cols, Mp, Kp, ldw, dx, dx_rows, splits, ldx;
-    float *scale, *dX;
+    float *scale, *dX, *dW;
     RowGrad *rows;
     uint16_t *Xm, *dZ, *Wm;
     size_t dx_stride, bytes;
@@ -551,7 +559,14 @@ struct FusedGradPlan {
         dZ = (uint16_t *)c.take((size_t)Mp * cols * 2);
         dX = (float *)c.take((size_t)splits * dx_stride * 4);
         Wm = (uint16_t *)c.take(copied ? (size_t)(flags & GEMM355_TRANS_B ? cols : Kp) * ldw * 2 : 0);
+        const bool tb = flags & GEMM355_TRANS_B;
+        dW = (float *)c.take(std::max(dw_bytes(tb, nc, K), N % cols != 0 ? dw_bytes(tb, N % cols, K) : 0));
         bytes = c.used;
+    }
+    // dW's partial sums for a piece of nc classes
+    size_t dw_bytes(bool tb, int nc, int K) const {
+        const int n = dw_splits(Mp, nc, K);
+        return n > 1 ? (size_t)n * (tb ? nc : K) * up((size_t)(tb ? K : nc), 4) * 4 : 0;
     }
 };
 
@@ -788,7 +803,12 @@ gemm355_status gradient_fused(const GradCall &a, bool copied, void *ws) {
             }
             G355_TRY(f16 ? launch_xent_dx_f16(p.dx, tb, q, a.s) : launch_xent_dx_bf16(p.dx, tb, q, a.s));
         }
-        const int dw_parts = a.dW != nullptr ? dw_sections(a.M, nc, a.K, part) : 0;
+        const int dw_ranges = dw_splits(p.Mp, nc, a.K);
+        int dw_parts = a.dW != nullptr ? dw_sections(a.M, nc, a.K, part) : 0;
+        if (dw_parts > 0 && dw_ranges > 1) {
+            part[0] = {0, nc, 128};
+            dw_parts = 1;
+        }
         for (int i = 0; i < dw_parts; ++i) {
             const Section &c = part[i];
             const int padded = (int)up((size_t)c.cols, 8);
@@ -806,7 +826,17 @@ gemm355_status gradient_fused(const GradCall &a, bool copied, void *ws) {
             q.out = (uint16_t *)at(a.dW, w_offset(a.flags, v0 + c.v0, a.lddw), 2);
             q.ldo = a.lddw;
             q.factor = p.scale + 1;
+            if (dw_ranges > 1) {
+                const Splits sp(p.Mp, dw_ranges);
+                q.splits = sp.count;
+                q.step = sp.step;
+                q.part = p.dW;
+                q.ldo = (int)up((size_t)q.cols, 4);
+                q.part_stride = (size_t)q.rows * q.ldo;
+            }
             G355_TRY(f16 ? launch_xent_dw_f16(c.tile, q, a.s) : launch_xent_dw_bf16(c.tile, q, a.s));
+            if (dw_ranges > 1)
+                G355_TRY(round16(a, q.rows, q.cols, p.dW, q.ldo, q.splits, q.part_stride, 0, p.scale, q.out, a.lddw));
         }
     }
     if (!one && a.dX != nullptr)
@@ -919,7 +949,7 @@ gemm355_status gemm355_xent(int dtype, unsigned flags, int M, int N, int K, cons
 }
 
 size_t gemm355_xent_grad_workspace(int dtype, unsigned flags, int M, int N, int K) {
-    if (!valid_shape(dtype, flags, M, N, K) || M == 0) return 0;
+    if (!valid_shape(dtype, flags, M, N, K) || M == 0 || K == 0) return 0;
     const size_t any = GradPlan(dtype, M, N, K, nullptr).bytes;
     if (!fused_shape(dtype, N, K)) return any;
     return std::max({any, FusedGradPlan(false, flags, M, N, K, nullptr).bytes,

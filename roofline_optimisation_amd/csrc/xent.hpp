@@ -75,8 +75,8 @@ struct ProductArgs {
 // kHead256 and kHead128.
 hipError_t launch_xent_dx_f16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s);
 hipError_t launch_xent_dx_bf16(int tile, bool b_mn, const ProductArgs &p, hipStream_t s);
-// dW's product: both operands m/n-contiguous, K a multiple of 128, 16-bit result.  Square
-// tiles of extent 128 or 256.
+// dW's product: both operands m/n-contiguous, K a multiple of 128; square tiles of extent 128
+// or 256 for the 16-bit result, 128 for partial sums (not accumulated).
 hipError_t launch_xent_dw_f16(int tile, const ProductArgs &p, hipStream_t s);
 hipError_t launch_xent_dw_bf16(int tile, const ProductArgs &p, hipStream_t s);
 

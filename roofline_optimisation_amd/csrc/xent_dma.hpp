@@ -321,17 +321,29 @@ void xent_dx_kernel(ProductArgs p, int words) {
     }
 }
 
-template <typename T, int E>
+// dW's product: the rounded result, or (PART) the partial sums of one of p.splits ranges of
+// the rows.
+template <typename T, int E, bool PART>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(E == 128 ? 2 : 1)))
 void xent_dw_kernel(ProductArgs p, int words) {
     using G = dma::Geo<E, E, 2, 2, 4, 0>;
-    using EX = RoundEpilogue<T>;
     __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
+    const int tiles = cdiv(p.rows, E) * cdiv(p.cols, E);
+    const int id = xcd_contiguous_id(blockIdx.x, gridDim.x), split = PART ? id / tiles : 0;
     int tm, tn;
-    grouped_tile(xcd_contiguous_id(blockIdx.x, gridDim.x), cdiv(p.rows, E), cdiv(p.cols, E), 4, tm, tn);
-    dma::dma_tile<T, true, true, 0, E, E, 2, 2, 4, 0, false, false, EX>(
-        p.M, p.N, p.K, p.A, p.lda, p.B, p.ldb, nullptr, 0, 1.0f, 0, tm * E, tn * E, lds,
-        EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
+    grouped_tile(id - split * tiles, cdiv(p.rows, E), cdiv(p.cols, E), 4, tm, tn);
+    if constexpr (PART) {
+        using EX = PartialEpilogue<T, 0>;
+        const int k0 = split * p.step, K = split + 1 < p.splits ? p.step : p.K - k0;
+        dma::dma_tile<T, true, true, 0, E, E, 2, 2, 4, 0, false, false, EX>(
+            p.M, p.N, K, p.A + (size_t)k0 * p.lda, p.lda, p.B + (size_t)k0 * p.ldb, p.ldb, nullptr, 0, 1.0f, 0, tm * E,
+            tn * E, lds, EX{p.rows, p.cols, p.part + split * p.part_stride, p.ldo});
+    } else {
+        using EX = RoundEpilogue<T>;
+        dma::dma_tile<T, true, true, 0, E, E, 2, 2, 4, 0, false, false, EX>(
+            p.M, p.N, p.K, p.A, p.lda, p.B, p.ldb, nullptr, 0, 1.0f, 0, tm * E, tn * E, lds,
+            EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
+    }
 }
 
 template <typename T, bool W_MN, int TILE, class EX>
@@ -394,9 +406,10 @@ hipError_t launch_dx(int tile, bool b_mn, const ProductArgs &p, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_dw(int tile, const ProductArgs &p, hipStream_t s) {
-    const dim3 grid(cdiv(p.rows, tile) * cdiv(p.cols, tile));
-    if (tile == 128) hipLaunchKernelGGL((xent_dw_kernel<T, 128>), grid, dim3(256), 0, s, p, word_stores(p));
-    else hipLaunchKernelGGL((xent_dw_kernel<T, 256>), grid, dim3(256), 0, s, p, word_stores(p));
+    const dim3 grid(cdiv(p.rows, tile) * cdiv(p.cols, tile) * (p.part != nullptr ? p.splits : 1));
+    if (p.part != nullptr) hipLaunchKernelGGL((xent_dw_kernel<T, 128, true>), grid, dim3(256), 0, s, p, 0);
+    else if (tile == 128) hipLaunchKernelGGL((xent_dw_kernel<T, 128, false>), grid, dim3(256), 0, s, p, word_stores(p));
+    else hipLaunchKernelGGL((xent_dw_kernel<T, 256, false>), grid, dim3(256), 0, s, p, word_stores(p));
     return hipGetLastError();
 }
 

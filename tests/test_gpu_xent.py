@@ -314,6 +314,32 @@ def test_no_rows():
         assert dX.shape == (0, 16) and dW.shape == (30, 16) and not dW.any()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [5, 700])
+def test_no_hidden_columns(dtype, N):
+    """K = 0: every logit is 0, and no gradient has elements."""
+    import torch
+    t = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    X, W = torch.empty(9, 0, device="cuda", dtype=t), torch.empty(N, 0, device="cuda", dtype=t)
+    y = torch.arange(9, device="cuda") % N
+    loss, lse = gb.linear_cross_entropy(X, W, y, trans_b=True)
+    # log N, to the rounding of the logarithm and the sum
+    assert ((loss.double() - np.log(N)).abs() <= 2.0 ** -20 * np.log(N)).all() and torch.equal(loss, lse)
+    dX, dW = gb.linear_cross_entropy_grad(X, W, y, lse, loss, trans_b=True)
+    assert dX.shape == (9, 0) and dW.shape == (N, 0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("trans_b", [True, False])
+@pytest.mark.parametrize("M,N,K", [(1500, 300, 136), (2300, 517, 264), (3000, 256, 100)])
+def test_many_rows_of_few_classes(M, N, K, dtype, trans_b):
+    """dW of few tiles, summed over ranges of the rows."""
+    X, W, y = ref.make_head(M, N, K, dtype, M)
+    h = Head(X, W, y, dtype, trans_b, padx=3, padw=1)
+    lse = check_xent(h, (M, N, K))
+    check_grad(h, lse, upstream(M, 1, dtype), (M, N, K), padx=1, padw=2)
+
+
 def test_repeated_calls_give_the_same_bits():
     for dtype in ("f32", "bf16"):
         X, W, y = ref.make_head(200, 3001, 256, dtype, 14)

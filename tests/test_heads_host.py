@@ -61,6 +61,8 @@ def test_workspace_sizes(dtype):
         assert f(dtype, gb.TRANS_B, 0, 10, 10) == 0
         assert f(dtype, gb.TRANS_B, 10, 0, 10) == 0
         assert f(3, 0, 10, 10, 10) == 0 and f(dtype, 4, 10, 10, 10) == 0 and f(dtype, 0, -1, 10, 10) == 0
+    assert gb.gemm355_xent_workspace(dtype, gb.TRANS_B, 10, 1000, 0) > 0
+    assert gb.gemm355_xent_grad_workspace(dtype, gb.TRANS_B, 10, 1000, 0) == 0   # no gradient has elements
     # never the whole logits: 8192 x 131072 of binary32 are 4 GiB
     assert gb.gemm355_xent_workspace(dtype, gb.TRANS_B, 8192, 131072, 4096) < 1 << 30
     assert gb.gemm355_xent_grad_workspace(dtype, gb.TRANS_B, 8192, 131072, 4096) < 4 << 30

@@ -480,8 +480,10 @@ struct StoreEpilogue {};
 // whole trip, every chunk at k >= K loads as zeros (DmaOp::issue), and the k-steps of the
 // last trip that lie wholly at k >= K are skipped.
 // EX: what becomes of the wave's accumulators: store_tile, or a functor of its own that is
-// called as ex.apply<EDGE>(acc, row0, col0), the wave's first row and column, with EDGE where
-// the tile reaches past ex.rows() or ex.cols() (M and N then only bound the loads).
+// called as ex.apply<EDGE>(acc, row0, col0, lds), the wave's first row and column, with EDGE
+// where the tile reaches past ex.rows() or ex.cols() (M and N then only bound the loads).
+// lds is the workgroup's ring, which other waves may still be reading: a functor that writes
+// to it begins with a barrier.
 template <typename T, bool A_MN, bool B_MN, int EPI, int EM, int EN, int WM, int WN, int NS, int PW,
           bool WHOLE = false, bool KR = false, class EX = StoreEpilogue>
 __device__ __forceinline__ void dma_tile(int M, int N, int K, const uint16_t *__restrict__ A, int lda,
@@ -713,9 +715,9 @@ __device__ __forceinline__ void dma_tile(int M, int N, int K, const uint16_t *__
     pin_acc(acc);
     if constexpr (!std::is_same<EX, StoreEpilogue>::value) {
         if (m0 + EM <= ex.rows() && n0 + EN <= ex.cols())
-            ex.template apply<false>(acc, m0 + wm * G::kTM, n0 + wn * G::kTN);
+            ex.template apply<false>(acc, m0 + wm * G::kTM, n0 + wn * G::kTN, lds_raw);
         else
-            ex.template apply<true>(acc, m0 + wm * G::kTM, n0 + wn * G::kTN);
+            ex.template apply<true>(acc, m0 + wm * G::kTM, n0 + wn * G::kTN, lds_raw);
     } else if (WHOLE || (m0 + EM <= M && n0 + EN <= N))
         store_tile<EPI, T, false>(acc, C, ldc, m0 + wm * G::kTM, n0 + wn * G::kTN, M, N, sign, flags);
     else

@@ -163,9 +163,18 @@ __global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int again
     float S = 1.0f;
     if (rescale) {
         float top = 0.0f;
-        for (int r = threadIdx.x; r < M; r += 256) {
-            const int64_t y = labels[r];
-            if (y != ignore && y >= 0 && y < N) top = fmaxf(top, fabsf(dloss[r]));
+        for (int r0 = threadIdx.x; r0 < M; r0 += 8 * 256) {   // eight rows' loads in flight
+            int64_t y[8];
+            float g[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int r = min(r0 + 256 * u, M - 1);   // the last row again: the same maximum
+                y[u] = labels[r];
+                g[u] = dloss[r];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (y[u] != ignore && y[u] >= 0 && y[u] < N) top = fmaxf(top, fabsf(g[u]));
         }
         for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 64));
         if (threadIdx.x % 64 == 0) sm[threadIdx.x / 64] = top;
@@ -218,47 +227,43 @@ __global__ __launch_bounds__(256) void xent_dz_kernel(int nc, int v0, const floa
 }
 
 // out = scale[1] * (the sum of `splits` partial sums, `stride` apart, and with `other` of those
-// that many elements further on), rounded to the 16-bit type; four columns per thread (VEC: in one access each).  Grid: (columns / 1024, rows).
+// that many elements further on), rounded to the 16-bit type; four columns per thread (VEC: loaded in one access; wide: stored in one).  Grid: (columns / 1024, rows).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *__restrict__ acc, int lda,
                                                          int splits, size_t stride, size_t other,
                                                          const float *__restrict__ scale, uint16_t *out,
-                                                         int ldo) {
+                                                         int ldo, int wide) {
     const int c = blockIdx.x * 1024 + 4 * (int)threadIdx.x;
     if (c >= cols) return;
     const float f = scale[1];
     const float *a = acc + (size_t)blockIdx.y * lda + c;
     uint16_t *o = out + (size_t)blockIdx.y * ldo + c;
-    if constexpr (VEC) {
+    if constexpr (VEC) {   // acc's rows hold cols rounded up to 4
         floatx4 v = *(const floatx4 *)a;
         int i = 1;
-        for (; i + 4 <= splits; i += 4) {   // four loads in flight, added in order
-            floatx4 w[4];
+        for (; i + 8 <= splits; i += 8) {   // eight loads in flight, added in order
+            floatx4 w[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) w[u] = *(const floatx4 *)(a + (i + u) * stride);
+            for (int u = 0; u < 8; ++u) w[u] = *(const floatx4 *)(a + (i + u) * stride);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v += w[u];
+            for (int u = 0; u < 8; ++u) v += w[u];
         }
         for (; i < splits; ++i) v += *(const floatx4 *)(a + i * stride);
-        if (other > 0) {
-            floatx4 w = *(const floatx4 *)(a + other);   // the remainders' sums, small ones
+        if (other > 0) {   // the remainders' sums
+            floatx4 w = *(const floatx4 *)(a + other);
 #pragma unroll 4
             for (int k = 1; k < splits; ++k) w += *(const floatx4 *)(a + other + k * stride);
             v += w;
         }
-        *(uint2 *)o = make_uint2((uint32_t)to_bits(f * v[0], T{}) | (uint32_t)to_bits(f * v[1], T{}) << 16,
-                                 (uint32_t)to_bits(f * v[2], T{}) | (uint32_t)to_bits(f * v[3], T{}) << 16);
-    } else {
-        for (int u = 0; u < 4 && c + u < cols; ++u) {
-            float v = a[u];
-            for (int i = 1; i < splits; ++i) v += a[i * stride + u];
-            if (other > 0) {
-                float w = a[other + u];
-                for (int i = 1; i < splits; ++i) w += a[other + i * stride + u];
-                v += w;
-            }
-            o[u] = to_bits(f * v, T{});
-        }
+        if (wide && c + 4 <= cols)
+            *(uint2 *)o = make_uint2((uint32_t)to_bits(f * v[0], T{}) | (uint32_t)to_bits(f * v[1], T{}) << 16,
+                                     (uint32_t)to_bits(f * v[2], T{}) | (uint32_t)to_bits(f * v[3], T{}) << 16);
+        else
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (c + u < cols) o[u] = to_bits(f * v[u], T{});
+    } else {               // one product's sums
+        for (int u = 0; u < 4 && c + u < cols; ++u) o[u] = to_bits(f * a[u], T{});
     }
 }
 
@@ -744,12 +749,14 @@ hipError_t piece_dz(const GradCall &a, const GradPlan &p, int v0, int nc) {
 
 hipError_t round16(const GradCall &a, int rows, int cols, const float *acc, int lda, int splits, size_t stride,
                    size_t other, const float *scale, void *out, int ldo) {
-    const bool vec = cols % 4 == 0 && lda % 4 == 0 && stride % 4 == 0 && other % 4 == 0 && ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
+    const bool vec = lda % 4 == 0 && stride % 4 == 0 && other % 4 == 0;
+    if (!vec && (splits > 1 || other > 0)) return hipErrorInvalidValue;
+    const int wide = ldo % 4 == 0 && (uintptr_t)out % 8 == 0;
     return over_rows(rows, [&](int r, int n) {
         const auto go = [&](auto t, auto v) {
             hipLaunchKernelGGL((xent_round_kernel<decltype(t), decltype(v)::value>), dim3(cdiv(cols, 1024), n),
                                dim3(256), 0, a.s, cols, acc + (size_t)r * lda, lda, splits, stride, other, scale,
-                               (uint16_t *)out + (size_t)r * ldo, ldo);
+                               (uint16_t *)out + (size_t)r * ldo, ldo, wide);
         };
         const auto typed = [&](auto t) { vec ? go(t, std::true_type{}) : go(t, std::false_type{}); };
         if (a.dtype == kF16) typed(f16_t{});

@@ -61,7 +61,7 @@ struct StatsEpilogue {
     __device__ int cols() const { return N; }
 
     template <bool EDGE, int kMB, int kNB>
-    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0, char *lds) const {
         const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4;
         float2 *const out = part + (size_t)(col0 / (16 * kNB)) * ldp;
         constexpr float kNegInf = -__builtin_huge_valf();
@@ -150,6 +150,28 @@ __device__ __forceinline__ uint32_t pair_word(float a0, float a1, int odd) {
     return (uint32_t)to_bits(lo, T{}) | ((uint32_t)to_bits(hi, T{}) << 16);
 }
 
+// 16 rows of a wave's 16-bit results, put together in its own part of LDS (rows of 16 kNB
+// elements and 16 bytes) so that they leave as 16-byte pieces of whole lines: as 4-byte words
+// out of the accumulators' layout each store instruction writes 64-byte pieces of four rows.
+template <int kNB>
+struct Strip {
+    static constexpr int kRow = 32 * kNB + 16;   // bytes
+    static constexpr int kChunks = 2 * kNB;      // 16-byte chunks of a row
+    char *base;
+    __device__ Strip(char *lds) : base(lds + (threadIdx.x / 64) * 16 * kRow) {}
+    // columns 2 c, 2 c + 1 of row r
+    __device__ __forceinline__ void put(int r, int c, uint32_t word) { *(uint32_t *)(base + r * kRow + 4 * c) = word; }
+    // store(r, c, v): chunk c of row r, each of them once
+    template <class F>
+    __device__ __forceinline__ void each(int lane, F store) {
+#pragma unroll
+        for (int k = 0; k < 16 * kChunks / 64; ++k) {
+            const int q = 64 * k + lane, r = q / kChunks, c = q % kChunks;
+            store(r, c, *(const u32x4 *)(base + r * kRow + 16 * c));
+        }
+    }
+};
+
 // dZ of the wave's tile: g (exp(z - lse) - [column is the label]), rounded to T.  Columns
 // from N to the next multiple of 8 are written as 0.  lo: the rounding's remainders, too.
 template <typename T>
@@ -162,9 +184,11 @@ struct DzEpilogue {
     __device__ int cols() const { return N; }
 
     template <bool EDGE, int kMB, int kNB>
-    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0, char *lds) const {
         const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4, odd = lane & 1;
         const int cw = col0 + (lane & 14) + 16 * odd, padded = (N + 7) & ~7;
+        Strip<kNB> strip(lds);
+        __syncthreads();
         // the data of a lane's next four rows are loaded while this quad row is computed
         floatx4 next[4];
         const auto load_rows = [&](int i) {
@@ -197,10 +221,8 @@ struct DzEpilogue {
                 }
                 const size_t at = (size_t)row * ldo + cw;
 #pragma unroll
-                for (int j = 0; j < kNB; j += 2) {
-                    const uint32_t v = pair_word<T>(d[j], d[j + 1], odd);
-                    if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(out + at + 16 * j) = v;
-                }
+                for (int j = 0; j < kNB; j += 2)
+                    strip.put(4 * q4 + r, (lane & 14) / 2 + 8 * (j + odd), pair_word<T>(d[j], d[j + 1], odd));
                 if (lo != nullptr) {
 #pragma unroll
                     for (int j = 0; j < kNB; j += 2) {
@@ -210,45 +232,49 @@ struct DzEpilogue {
                     }
                 }
             }
+            strip.each(lane, [&](int r, int c, u32x4 v) {
+                const int row = row0 + 16 * i + r, col = col0 + 8 * c;
+                if (!EDGE || (row < M && col < padded)) *(u32x4 *)(out + (size_t)row * ldo + col) = v;
+            });
         }
     }
 };
 
-// The 16-bit result of a product: round(factor * sum), in 4-byte words where the output
-// allows them.
+// The 16-bit result of a product: round(factor * sum), in 16-byte pieces at whatever alignment
+// the output has (gfx950 under the HSA ABI runs with unaligned global access enabled).
 template <typename T>
 struct RoundEpilogue {
     int nrows, ncols;
     uint16_t *out;
-    int ldo, words;
+    int ldo;
     const float *factor;
     __device__ int rows() const { return nrows; }
     __device__ int cols() const { return ncols; }
 
     template <bool EDGE, int kMB, int kNB>
-    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
-        const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4, odd = lane & 1;
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0, char *lds) const {
+        const int lane = dma::lane_here(), q4 = lane >> 4, odd = lane & 1;
         const float f = *factor;
-        const int cw = words ? col0 + (lane & 14) + 16 * odd : col0 + c16;
+        Strip<kNB> strip(lds);
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kMB; ++i)
+        for (int i = 0; i < kMB; ++i) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = row0 + 16 * i + 4 * q4 + r;
-                uint16_t *o = out + (size_t)row * ldo + cw;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int j = 0; j < kNB; j += 2) {
-                    const float a0 = f * acc_read(acc[i][j][r]), a1 = f * acc_read(acc[i][j + 1][r]);
-                    if (words) {
-                        const uint32_t v = pair_word<T>(a0, a1, odd);
-                        if (!EDGE || (row < nrows && cw + 16 * j + 1 < ncols)) *(uint32_t *)(o + 16 * j) = v;
-                        else if (row < nrows && cw + 16 * j < ncols) o[16 * j] = (uint16_t)v;
-                    } else {
-                        if (!EDGE || (row < nrows && cw + 16 * j < ncols)) o[16 * j] = to_bits(a0, T{});
-                        if (!EDGE || (row < nrows && cw + 16 * j + 16 < ncols)) o[16 * j + 16] = to_bits(a1, T{});
-                    }
-                }
-            }
+                for (int j = 0; j < kNB; j += 2)
+                    strip.put(4 * q4 + r, (lane & 14) / 2 + 8 * (j + odd),
+                              pair_word<T>(f * acc_read(acc[i][j][r]), f * acc_read(acc[i][j + 1][r]), odd));
+            strip.each(lane, [&](int r, int c, u32x4 v) {
+                const int row = row0 + 16 * i + r, col = col0 + 8 * c;
+                uint16_t *o = out + (size_t)row * ldo + col;
+                if (!EDGE || (row < nrows && col + 8 <= ncols)) *(u16x8_ua *)o = __builtin_bit_cast(u16x8, v);
+                else if (row < nrows)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (col + e < ncols) o[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+            });
+        }
     }
 };
 
@@ -262,7 +288,7 @@ struct PartialEpilogue {
     __device__ int cols() const { return ncols; }
 
     template <bool EDGE, int kMB, int kNB>
-    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0) const {
+    __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0, char *lds) const {
         dma::store_tile<EPI, T, EDGE>(acc, part, ldo, row0, col0, nrows, ncols, 1.0f, EPI);
     }
 };
@@ -296,7 +322,7 @@ void xent_head_kernel(int M, int N, int K, const uint16_t *__restrict__ X, int l
 // there, 1), or the rounded result.
 template <typename T, bool B_MN, int TILE, bool KR, int EPI>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(HeadTile<TILE>::kPerSimd)))
-void xent_dx_kernel(ProductArgs p, int words) {
+void xent_dx_kernel(ProductArgs p) {
     using H = HeadTile<TILE>;
     constexpr int EM = H::kEM, EN = H::kEN;
     __shared__ __attribute__((aligned(1024))) char lds[H::G::kLds];
@@ -317,7 +343,7 @@ void xent_dx_kernel(ProductArgs p, int words) {
         using EX = RoundEpilogue<T>;
         dma::dma_tile<T, false, B_MN, 0, EM, EN, H::kWM, H::kWN, H::kNs, 0, false, KR, EX>(
             p.M, p.N, K, A, p.lda, B, p.ldb, nullptr, 0, 1.0f, 0, tm * EM, tn * EN, lds,
-            EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
+            EX{p.rows, p.cols, p.out, p.ldo, p.factor});
     }
 }
 
@@ -325,7 +351,7 @@ void xent_dx_kernel(ProductArgs p, int words) {
 // the rows.
 template <typename T, int E, bool PART>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(E == 128 ? 2 : 1)))
-void xent_dw_kernel(ProductArgs p, int words) {
+void xent_dw_kernel(ProductArgs p) {
     using G = dma::Geo<E, E, 2, 2, 4, 0>;
     __shared__ __attribute__((aligned(1024))) char lds[G::kLds];
     const int tiles = cdiv(p.rows, E) * cdiv(p.cols, E);
@@ -342,7 +368,7 @@ void xent_dw_kernel(ProductArgs p, int words) {
         using EX = RoundEpilogue<T>;
         dma::dma_tile<T, true, true, 0, E, E, 2, 2, 4, 0, false, false, EX>(
             p.M, p.N, p.K, p.A, p.lda, p.B, p.ldb, nullptr, 0, 1.0f, 0, tm * E, tn * E, lds,
-            EX{p.rows, p.cols, p.out, p.ldo, words, p.factor});
+            EX{p.rows, p.cols, p.out, p.ldo, p.factor});
     }
 }
 
@@ -376,17 +402,15 @@ hipError_t launch_head(int tile, const HeadArgs &h, const EX &ex, hipStream_t s)
     return h.trans_b ? launch_head_layout<T, false>(tile, h, ex, s) : launch_head_layout<T, true>(tile, h, ex, s);
 }
 
-inline int word_stores(const ProductArgs &p) { return p.ldo % 2 == 0 && (uintptr_t)p.out % 4 == 0; }
-
 template <typename T, bool B_MN, int TILE, bool KR>
 hipError_t launch_dx_epi(const ProductArgs &p, hipStream_t s) {
     const dim3 grid(cdiv(p.rows, kHeadRows[TILE]) * cdiv(p.cols, kHeadCols[TILE]) * p.splits);
     if (p.part == nullptr)
-        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 2>), grid, dim3(256), 0, s, p, word_stores(p));
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 2>), grid, dim3(256), 0, s, p);
     else if (p.accumulate)
-        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 1>), grid, dim3(256), 0, s, p, 0);
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 1>), grid, dim3(256), 0, s, p);
     else
-        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 0>), grid, dim3(256), 0, s, p, 0);
+        hipLaunchKernelGGL((xent_dx_kernel<T, B_MN, TILE, KR, 0>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -407,9 +431,9 @@ hipError_t launch_dx(int tile, bool b_mn, const ProductArgs &p, hipStream_t s) {
 template <typename T>
 hipError_t launch_dw(int tile, const ProductArgs &p, hipStream_t s) {
     const dim3 grid(cdiv(p.rows, tile) * cdiv(p.cols, tile) * (p.part != nullptr ? p.splits : 1));
-    if (p.part != nullptr) hipLaunchKernelGGL((xent_dw_kernel<T, 128, true>), grid, dim3(256), 0, s, p, 0);
-    else if (tile == 128) hipLaunchKernelGGL((xent_dw_kernel<T, 128, false>), grid, dim3(256), 0, s, p, word_stores(p));
-    else hipLaunchKernelGGL((xent_dw_kernel<T, 256, false>), grid, dim3(256), 0, s, p, word_stores(p));
+    if (p.part != nullptr) hipLaunchKernelGGL((xent_dw_kernel<T, 128, true>), grid, dim3(256), 0, s, p);
+    else if (tile == 128) hipLaunchKernelGGL((xent_dw_kernel<T, 128, false>), grid, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((xent_dw_kernel<T, 256, false>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

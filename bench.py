@@ -15,6 +15,9 @@ management's transient instead of the kernel.  The FP16-input / FP32-accumulate 
 logits per workload) and prints one JSON line for the 16384 x 4096 workload, with its
 roofline against the 8 TB/s HBM peak and the CPU oracle's rate beside it.
 
+`--heads PATH` measures the softmax cross entropy of a projection, its gradient, routing to
+experts and its gradient instead, and writes a markdown table to PATH (no JSON line).
+
 The JSON line also carries
   * "roofline": the dominant kernel's achieved TFLOP/s against the MI355X peak for its
     arithmetic (FP32 on the matrix cores: 157.3 TFLOP/s), with HBM traffic from the
@@ -723,6 +726,88 @@ def softmax_lines(res):
     return lines
 
 
+# (operator, dtype, rows, classes or experts, hidden size, W as N x K) of --heads
+HEAD_SHAPES = [("loss", "bf16", 16, 32000, 2048, True), ("loss", "f16", 2047, 50003, 2048, True),
+               ("loss", "f32", 1000, 32000, 1024, False), ("loss", "bf16", 8192, 131072, 4096, True),
+               ("gradient", "f16", 512, 32000, 1024, True), ("gradient", "bf16", 2047, 32000, 2048, False),
+               ("gradient", "bf16", 4096, 50003, 2048, True), ("gradient", "bf16", 8192, 131072, 4096, True),
+               ("routes", "bf16", 8, 128, 0, True), ("routes in groups", "f32", 16384, 256, 0, True),
+               ("route gradient", "f32", 16384, 256, 0, True), ("route gradient, dense", "bf16", 4095, 64, 0, True)]
+
+
+def heads_measure(warm=10, reps=20):
+    """Per-call time of the loss and routing wrappers on HEAD_SHAPES (host work included),
+    three sets of inputs in turn (one for the largest), and the rates of what a call cannot
+    do without: each operand read and each result written once, 2MNK FLOPs a product."""
+    import torch
+
+    from roofline_optimisation_amd import binding as gb
+
+    types = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+    out = []
+    for op, dtype, M, N, K, tb in HEAD_SHAPES:
+        g = torch.Generator(device="cuda").manual_seed(11)
+        t, b = types[dtype], 4 if dtype == "f32" else 2
+        calls = []
+        for _ in range(1 if K and N * K > 1 << 28 else 3):
+            if K:
+                X = torch.randn(M, K, generator=g, device="cuda").to(t)
+                W = (torch.randn(*((N, K) if tb else (K, N)), generator=g, device="cuda") / K ** 0.5).to(t)
+                y = torch.randint(0, N, (M,), generator=g, device="cuda")
+                if op == "loss":
+                    calls.append(lambda X=X, W=W, y=y: gb.linear_cross_entropy(X, W, y, trans_b=tb))
+                else:
+                    lse = gb.linear_cross_entropy(X, W, y, trans_b=tb)[1]
+                    d = torch.full((M,), 1.0 / M, device="cuda")
+                    calls.append(lambda X=X, W=W, y=y, lse=lse, d=d: gb.linear_cross_entropy_grad(
+                        X, W, y, lse, d, trans_b=tb))
+                continue
+            x = (1.5 * torch.randn(M, N, generator=g, device="cuda")).to(t)
+            k = 6 if "dense" in op else 8
+            kw = dict(score="sigmoid", renorm=True, scale=2.5) if dtype == "f32" else \
+                dict(renorm="dense" not in op)
+            if op.startswith("routes"):
+                if "groups" in op:
+                    kw.update(bias=0.1 * torch.randn(N, generator=g, device="cuda"), groups=8, top_groups=4, group_top=2)
+                calls.append(lambda x=x, kw=kw: gb.route(x, k, **kw))
+            else:
+                ids = torch.sort(x.float(), dim=1, descending=True)[1][:, :k].int().contiguous()
+                d = torch.randn(M, k, generator=g, device="cuda")
+                calls.append(lambda x=x, ids=ids, d=d, kw=kw: gb.route_grad(x, ids, d, **kw))
+        for i in range(warm):
+            calls[i % len(calls)]()
+        a, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        rounds = []
+        for _ in range(3):
+            torch.cuda.synchronize()
+            a.record()
+            for i in range(reps):
+                calls[i % len(calls)]()
+            e.record()
+            torch.cuda.synchronize()
+            rounds.append(a.elapsed_time(e) / reps)
+        ms = sorted(rounds)[1]
+        flops = 0 if not K else (2 if op == "loss" else 6) * M * N * K
+        k = 6 if "dense" in op else 8
+        nbytes = (M * K + N * K) * b * (1 if op == "loss" else 2) if K else M * N * b * (1 if op.startswith("routes") else 2) + 8 * M * k
+        out.append((op, dtype, M, N, K, tb, ms, flops / ms / 1e9, nbytes / ms / 1e6))
+        log(f"[heads] {op} {dtype} {M}x{N}x{K}: {ms * 1e3:.1f} us, {flops / ms / 1e9:.0f} TFLOP/s, {nbytes / ms / 1e6:.0f} GB/s")
+        del calls
+    return out
+
+
+def heads_lines(res):
+    lines = ["# libgemm355 vocabulary and router heads on one MI355X", "",
+             "Per call through the torch wrappers, host work included (HIP events, median of 3 rounds of",
+             "20 calls after 10 warm-up calls); three sets of inputs in turn, one for the largest.", "",
+             "| operator | dtype | rows | classes / experts | hidden | W | us | TFLOP/s | GB/s |",
+             "|---|---|---|---|---|---|---|---|---|"]
+    for op, dtype, M, N, K, tb, ms, tf, gbs in res:
+        lines.append(f"| {op} | {dtype} | {M} | {N} | {K or '-'} | {('N x K' if tb else 'K x N') if K else '-'} | "
+                     f"{ms * 1e3:.1f} | {f'{tf:.0f}' if tf else '-'} | {gbs:.0f} |")
+    return lines
+
+
 def softmax_cpu_baseline(X, min_seconds=10.0):
     """The oracle's softmax on this host: the first 1024 rows of the workload, repeated
     until at least `min_seconds` of wall time, as algorithmic GB/s (8 bytes per element)."""
@@ -964,6 +1049,9 @@ def main():
                     help="only measure the row-wise softmax and row sum on their 64 Mi-element "
                          "workloads, write the markdown table to PATH and print one JSON line "
                          "for the 16384 x 4096 workload; no GEMM timing")
+    ap.add_argument("--heads", default=None, metavar="PATH",
+                    help="only measure the cross entropy of a projection, routing to experts and "
+                         "their gradients, and write the markdown table to PATH; no JSON line")
     ap.add_argument("--family", choices=["naive", "lds_tiled", "regblock", "mfma", "mfma_split",
                                          "mfma_w8", "mfma_t256x128", "mfma_t256x256", "mfma_staged128", "mfma_staged_small"], default=None,
                     help="only launch one kernel family (--warmup untimed and --steps timed "
@@ -1046,6 +1134,13 @@ def main():
         with open(args.schedules, "w") as f:
             f.write("\n".join(schedule_lines(warm=max(args.warmup, 1))) + "\n")
         log(f"[bench] schedule table written to {args.schedules}")
+        return
+
+    if args.heads:
+        res = heads_measure()
+        with open(args.heads, "w") as f:
+            f.write("\n".join(heads_lines(res)) + "\n")
+        log(f"[bench] heads table written to {args.heads}")
         return
 
     if args.softmax:

@@ -140,14 +140,27 @@ struct StatsEpilogue {
     }
 };
 
-// One row of a pair of quads as 4-byte words of two 16-bit values: lanes 2m and 2m + 1
-// exchange a register, the even lane gets columns 2m, 2m + 1 of the first quad, the odd lane
-// those of the second.
+// Two values rounded to the 16-bit type, the first in the low half.
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 template <typename T>
-__device__ __forceinline__ uint32_t pair_word(float a0, float a1, int odd) {
-    const float other = of_lane<kDppQuadXor1>(odd ? a0 : a1);
-    const float lo = odd ? other : a0, hi = odd ? a1 : other;
-    return (uint32_t)to_bits(lo, T{}) | ((uint32_t)to_bits(hi, T{}) << 16);
+__device__ __forceinline__ uint32_t round_pair(float a, float b) {
+    if constexpr (std::is_same<T, bf16_t>::value)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), bf16x2));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), halfx2));
+}
+
+// One row of a pair of quads as 4-byte words of two 16-bit values: lanes 2m and 2m + 1
+// exchange their rounded pairs, the even lane keeps columns 2m, 2m + 1 of the first quad (the
+// low halves), the odd lane those of the second.  sel: pair_select(odd).
+__device__ __forceinline__ uint32_t pair_select(int odd) { return odd ? 0x03020706u : 0x05040100u; }
+template <typename T>
+__device__ __forceinline__ uint32_t pair_word(float a0, float a1, uint32_t sel) {
+    const uint32_t own = round_pair<T>(a0, a1);
+    const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, kDppQuadXor1, 0xF, 0xF, true);
+    return __builtin_amdgcn_perm(other, own, sel);
 }
 
 // 16 rows of a wave's 16-bit results, put together in its own part of LDS (rows of 16 kNB
@@ -187,6 +200,7 @@ struct DzEpilogue {
     __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0, char *lds) const {
         const int lane = dma::lane_here(), c16 = lane & 15, q4 = lane >> 4, odd = lane & 1;
         const int cw = col0 + (lane & 14) + 16 * odd, padded = (N + 7) & ~7;
+        const uint32_t sel = pair_select(odd);
         Strip<kNB> strip(lds);
         __syncthreads();
         // the data of a lane's next four rows are loaded while this quad row is computed
@@ -206,29 +220,45 @@ struct DzEpilogue {
             for (int r = 0; r < 4; ++r) now[r] = next[r];
             if (i + 1 < kMB) load_rows(i + 1);
             __builtin_amdgcn_sched_barrier(0);
+            float d[4][kNB];
+            int hot[4];   // the label's column relative to the lane's first
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = row0 + 16 * i + 4 * q4 + r;
                 const RowGrad w = __builtin_bit_cast(RowGrad, now[r]);
-                const int hot = w.label - v0 - col0 - c16;
                 const float shift = -w.lse * kLog2e;
-                float d[kNB];
+                hot[r] = w.label - v0 - col0 - c16;
 #pragma unroll
-                for (int j = 0; j < kNB; ++j) {
-                    const float p = __builtin_amdgcn_exp2f(fmaf(acc_read(acc[i][j][r]), kLog2e, shift));
-                    d[j] = fmaf(w.g, p, hot == 16 * j ? -w.g : 0.0f);
-                    if (EDGE && col0 + 16 * j + c16 >= N) d[j] = 0.0f;
+                for (int j = 0; j < kNB; ++j)
+                    d[r][j] = w.g * __builtin_amdgcn_exp2f(fmaf(acc_read(acc[i][j][r]), kLog2e, shift));
+            }
+            // - g at the labels' columns: of rows of many columns few tiles hold any
+            const unsigned last = 16 * (kNB - 1);
+            if (__any((unsigned)hot[0] <= last || (unsigned)hot[1] <= last || (unsigned)hot[2] <= last ||
+                      (unsigned)hot[3] <= last)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j)
+                        if (hot[r] == 16 * j) d[r][j] -= __builtin_bit_cast(RowGrad, now[r]).g;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (EDGE) {
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j)
+                        if (col0 + 16 * j + c16 >= N) d[r][j] = 0.0f;
                 }
-                const size_t at = (size_t)row * ldo + cw;
 #pragma unroll
                 for (int j = 0; j < kNB; j += 2)
-                    strip.put(4 * q4 + r, (lane & 14) / 2 + 8 * (j + odd), pair_word<T>(d[j], d[j + 1], odd));
+                    strip.put(4 * q4 + r, (lane & 14) / 2 + 8 * (j + odd), pair_word<T>(d[r][j], d[r][j + 1], sel));
                 if (lo != nullptr) {
+                    const int row = row0 + 16 * i + 4 * q4 + r;
 #pragma unroll
                     for (int j = 0; j < kNB; j += 2) {
-                        const uint32_t v = pair_word<T>(d[j] - to_float(T{to_bits(d[j], T{})}),
-                                                        d[j + 1] - to_float(T{to_bits(d[j + 1], T{})}), odd);
-                        if (!EDGE || (row < M && cw + 16 * j < padded)) *(uint32_t *)(lo + at + 16 * j) = v;
+                        const uint32_t v = pair_word<T>(d[r][j] - to_float(T{to_bits(d[r][j], T{})}),
+                                                        d[r][j + 1] - to_float(T{to_bits(d[r][j + 1], T{})}), sel);
+                        if (!EDGE || (row < M && cw + 16 * j < padded))
+                            *(uint32_t *)(lo + (size_t)row * ldo + cw + 16 * j) = v;
                     }
                 }
             }
@@ -255,6 +285,7 @@ struct RoundEpilogue {
     __device__ __forceinline__ void apply(floatx4 (&acc)[kMB][kNB], int row0, int col0, char *lds) const {
         const int lane = dma::lane_here(), q4 = lane >> 4, odd = lane & 1;
         const float f = *factor;
+        const uint32_t sel = pair_select(odd);
         Strip<kNB> strip(lds);
         __syncthreads();
 #pragma unroll
@@ -264,7 +295,7 @@ struct RoundEpilogue {
 #pragma unroll
                 for (int j = 0; j < kNB; j += 2)
                     strip.put(4 * q4 + r, (lane & 14) / 2 + 8 * (j + odd),
-                              pair_word<T>(f * acc_read(acc[i][j][r]), f * acc_read(acc[i][j + 1][r]), odd));
+                              pair_word<T>(f * acc_read(acc[i][j][r]), f * acc_read(acc[i][j + 1][r]), sel));
             strip.each(lane, [&](int r, int c, u32x4 v) {
                 const int row = row0 + 16 * i + r, col = col0 + 8 * c;
                 uint16_t *o = out + (size_t)row * ldo + col;

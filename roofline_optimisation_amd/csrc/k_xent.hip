@@ -8,8 +8,17 @@
 // piece, rounded to the operands' type, is the left operand of dX += dZ.op(W)^T and of the
 // piece's columns (or rows) of dW = X^T.dZ.
 //
-// This file: the rows' kernels, the plan that lays out a call's workspace, and the entry
-// points.  The products run in this library's GEMM kernels.
+// Two paths.  16-bit types with 256 classes or more run on the direct-to-LDS tiles with
+// epilogues of their own (xent_dma.hpp): the forward pass writes one (maximum, sum) pair per
+// row and 32 to 128 classes, the backward pass dZ of a piece of the vocabulary (512 MiB at
+// most) and two products that read it; what those tiles cannot load where it lies (rows not
+// 16-byte aligned, K not a multiple of 8) is copied to aligned rows first, W a piece of 128
+// MiB at a time.  Everything else (binary32; few classes) writes a piece of binary32 logits
+// with the library's GEMM kernels and reads it back.
+//
+// This file: the rows' kernels, the plans that lay out a call's workspace, and the entry
+// points.  Every kernel here is bound by memory; all of them together take 1-2 % of a large
+// call and half of the smallest ones (4-5 us each, launch included).
 #include <algorithm>
 
 #include "../../include/gemm355_softmax.h"
@@ -227,7 +236,8 @@ __global__ __launch_bounds__(256) void xent_dz_kernel(int nc, int v0, const floa
 }
 
 // out = scale[1] * (the sum of `splits` partial sums, `stride` apart, and with `other` of those
-// that many elements further on), rounded to the 16-bit type; four columns per thread (VEC: loaded in one access; wide: stored in one).  Grid: (columns / 1024, rows).
+// that many elements further on), rounded to the 16-bit type; four columns per thread (VEC:
+// loaded in one access; wide: stored in one).  Grid: (columns / 1024, rows).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *__restrict__ acc, int lda,
                                                          int splits, size_t stride, size_t other,
@@ -354,7 +364,9 @@ struct GradPlan {
     GradPlan(int dtype, int M, int N, int K, void *ws) {
         const bool h16 = dtype != kF32;
         const size_t es = h16 ? 2 : 4;
-        Mp = h16 ? M : (int)up((size_t)M, 32);
+        // binary32: dW over 294 rows of 11483 x 2944 258 us, over 320 238; a few rows gain
+        // nothing from it and pay for writing more logits (5 x 11952 x 3973 270 us, 32 rows 310)
+        Mp = h16 || M <= 64 ? M : (int)up((size_t)M, 32);
         cols = piece_cols(Mp, N);
         ldm = (int)up((size_t)(K > 0 ? K : 1), 16 / es);
         ranges = step = 0;
@@ -401,11 +413,12 @@ bool weights_load(unsigned flags, int N, int K, const void *W, int ldw) {
 // The time of M x N logits in one kind of tile, in rounds of 256 x 256 tiles (one per CU):
 // rounds of resident tiles times what a round takes, measured at K = 2048 (bf16, us: 256 x
 // 256 46, 128 x 256 33, 64 x 256 29 with one per CU and 60 with two, 64 x 128 12, 64 x 64 8
-// and 14, 128 x 128 17 and 30).  Few rows are bound by reading W, for which many small tiles do best: 16 x 32000 x
-// 2048 51 / 41 / 38 / 26 / 26 us in this order, 256 x 8000 x 2048 48 / 36 / 32 / 17 / 21,
-// 256 x 32000 x 2048 54 / 43 / 44 / 52 / 59, 512 x 32000 x 1024 37 / 45 / 47.  128 x 128 two
-// per CU has neither the largest tile's rate nor its last rows' waste: 276 x 104940 x 640 72
-// against 78 us in 128 x 256 and 92 in 256 x 256, 4096 x 32000 x 2048 474 against 392.
+// and 14, 128 x 128 17 and 30).  Few rows are bound by reading W, for which many small tiles
+// do best: 16 x 32000 x 2048 51 / 41 / 38 / 26 / 26 us in this order, 256 x 8000 x 2048 48 /
+// 36 / 32 / 17 / 21, 256 x 32000 x 2048 54 / 43 / 44 / 52 / 59, 512 x 32000 x 1024 37 / 45 /
+// 47.  128 x 128 two per CU has neither the largest tile's rate nor its last rows' waste: 276
+// x 104940 x 640 72 against 78 us in 128 x 256 and 92 in 256 x 256, 4096 x 32000 x 2048 474
+// against 392.
 double head_cost(int tile, int M, int N) {
     constexpr double kOne[kHeadTiles] = {1.0, 0.72, 0.63, 0.27, 0.17, 0.36};
     constexpr double kTwo[kHeadTiles] = {0, 0, 1.2, 0, 0.3, 0.6};

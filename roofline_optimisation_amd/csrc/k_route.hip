@@ -5,20 +5,25 @@
 // optimisation); the choice adds a bias, keeps the best groups and takes the k best, ties
 // to the lowest index.
 //
-// One wave takes a row, Q = experts / 64 of its experts per lane.  A row is a few hundred
+// One wave takes a row, Q = experts / 64 neighbouring ones per lane.  A row is a few hundred
 // bytes, so the time goes into instructions, not memory.  The ids are whole numbers and have
 // to be those of exact scores, but only rows with two candidates closer than binary32 can
 // tell apart need better: a row is first decided on 32-bit keys (the logits themselves where
 // no bias is added, so exactly; else binary32 scores plus bias), and where two neighbours of
 // the resulting order, or two groups, are closer than the bound of the scores' error, the
-// row is decided again on binary64 scores.  Each round takes the largest key (a maximum over
-// registers, four register exchanges within 16 lanes, a scalar maximum of four lanes) and
-// the lowest expert that holds it (a ballot per register).
+// row is decided again on binary64 scores.  Each lane sorts its keys; a round then takes the
+// largest first key (four register exchanges within 16 lanes, a scalar maximum of four lanes)
+// and the lowest lane that holds it (a ballot), whose next key moves up.
 //
-// Bound by the vector unit: about 660 instructions a row of 256 experts in groups with a bias
-// and 8 places (binary64 throughout: over 2000).  16384 such rows take 36 us (29 without the
-// counts, whose per-workgroup sums are added to memory by atomics; whole numbers, so in any
-// order), 15 us without groups and bias; reading the logits alone would take 4.
+// Bound by instructions, of which the vector and the scalar unit take about as many (binary64
+// throughout: four times as many).  16384 rows of 256 experts in groups with a bias and 8
+// places take 24.4 us, their counts 3.9 more; 10 us without groups and bias, where reading the
+// logits alone would take 4.  With rounds that look through all of a lane's keys, groups
+// ranked one after the other, the weights of one row at a time and counts added up by each
+// workgroup's atomics it was 36.  Registers (88) leave five waves on a SIMD; a bound of six
+// makes the compiler spill.
+#include <algorithm>
+
 #include "../../include/gemm355_softmax.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -138,21 +143,27 @@ __device__ __forceinline__ float exchange(float v) { return X::get(v); }
 template <class X>
 __device__ __forceinline__ double exchange(double v) { return exchange64<X>(v); }
 
-// A group's score, in every one of its lanes: group g of `per` experts (choices in LDS) is
-// scanned by the S = 64 / (groups rounded up to a power of two) lanes from g S on.
+// A group's score, in every one of its S lanes (a power of two, aligned), from the two largest
+// choices that each of them has seen.
 template <typename F>
-__device__ __forceinline__ F group_score(const F *choice, int per, int S, int sub, int group_top) {
-    constexpr F low = (F)kLow;
-    F best = low, second = low;
-#pragma unroll 1
-    for (int i = sub; i < per; i += S) merge_two(best, second, choice[i], low);
+__device__ __forceinline__ F group_score(F best, F second, int S, int group_top) {
     if (S > 1) merge_two(best, second, exchange<DppXchg<kDppQuadXor1>>(best), exchange<DppXchg<kDppQuadXor1>>(second));
     if (S > 2) merge_two(best, second, exchange<DppXchg<kDppQuadXor2>>(best), exchange<DppXchg<kDppQuadXor2>>(second));
     if (S > 4)
         merge_two(best, second, exchange<DppXchg<kDppRowHalfMirror>>(best), exchange<DppXchg<kDppRowHalfMirror>>(second));
     if (S > 8) merge_two(best, second, exchange<DppXchg<kDppRowMirror>>(best), exchange<DppXchg<kDppRowMirror>>(second));
     if (S > 16) merge_two(best, second, exchange<SwapHalves16>(best), exchange<SwapHalves16>(second));
-    return group_top == 2 && second > low ? best + second : best;
+    return group_top == 2 && second > (F)kLow ? best + second : best;
+}
+
+// The same for a group of `per` experts whose choices lie in LDS, scanned by its S lanes.
+template <typename F>
+__device__ __forceinline__ F group_score(const F *choice, int per, int S, int sub, int group_top) {
+    constexpr F low = (F)kLow;
+    F best = low, second = low;
+#pragma unroll 1
+    for (int i = sub; i < per; i += S) merge_two(best, second, choice[i], low);
+    return group_score(best, second, S, group_top);
 }
 
 __device__ __forceinline__ float lane_value(float v, int lane) { return read_lane(v, lane); }
@@ -163,29 +174,28 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
                                               << 32);
 }
 
-// Which of the groups are among the `top` of the largest score, ties to the lowest group;
-// near: a kept score lies within `margin` of one that is not.  A lane holds the score of
-// group lane >> shift.
+// Which of the groups are among the `top` of the largest score, ties to the lowest group, as
+// the lanes of those groups; near: a kept score lies within `margin` of one that is not.  A
+// lane holds the score of group lane >> shift (shift < 6), and compares it with that of every
+// 2^shift-th group.
 template <typename F>
 __device__ __forceinline__ unsigned long long best_groups(F score, int groups, int top, int shift, F margin,
                                                           bool &near) {
-    const int mine = (int)(threadIdx.x % 64) >> shift;
+    const int lane = threadIdx.x % 64, mine = lane >> shift, S = 1 << shift, first = lane & -S;
+    const uint32_t group_lanes = 0xffffffffu >> (32 - S);
     int rank = 0;
     int close = 0;   // groups ahead of mine by no more than the margin
 #pragma unroll 1
-    for (int g = 0; g < groups; ++g) {
-        const F o = lane_value(score, g << shift);
-        const bool ahead = o > score || (o == score && g < mine);
-        rank += ahead;
-        close += ahead && o - score <= margin;
+    for (int g0 = 0; g0 < groups; g0 += S) {
+        const int g = g0 + (lane & (S - 1));
+        const F o = __shfl(score, (g << shift) & 63, 64);
+        const bool ahead = g < groups && (o > score || (o == score && g < mine));
+        rank += __builtin_popcount((uint32_t)(__ballot(ahead) >> first) & group_lanes);
+        close += __builtin_popcount((uint32_t)(__ballot(ahead && o - score <= margin) >> first) & group_lanes);
     }
     // not kept, and one that is (ranks below top) among those just ahead
     near = __any(mine < groups && rank >= top && rank - close < top);
-    const unsigned long long in = __ballot(rank < top);   // 2^shift lanes a group
-    unsigned long long kept = 0;
-#pragma unroll 1
-    for (int g = 0; g < groups; ++g) kept |= ((in >> (g << shift)) & 1) << g;
-    return kept;
+    return __ballot(mine < groups && rank < top);
 }
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -199,12 +209,19 @@ __device__ __forceinline__ void wave_lds_sync() {
 // is below 2^-57), times 2^n.  The coefficients 1 / 13!, 1 / 12!, ... 1 lie in LDS: held in
 // registers across a kernel's loop over rows they take 28 scalar ones.
 constexpr int kTaylor = 14;
-__device__ __forceinline__ void taylor_to_lds(double *coef) {
-    if (threadIdx.x < kTaylor) {
+struct TaylorTable {
+    double v[kTaylor];
+    constexpr TaylorTable() : v{} {
         double f = 1.0;
-        for (int i = kTaylor - 1 - (int)threadIdx.x; i > 1; --i) f *= (double)i;
-        coef[threadIdx.x] = 1.0 / f;
+        for (int n = 0; n < kTaylor; ++n) {
+            f *= n > 1 ? (double)n : 1.0;
+            v[kTaylor - 1 - n] = 1.0 / f;
+        }
     }
+};
+__constant__ const TaylorTable kTaylorTable;
+__device__ __forceinline__ void taylor_to_lds(double *coef) {
+    if (threadIdx.x < kTaylor) coef[threadIdx.x] = kTaylorTable.v[threadIdx.x];
 }
 __device__ __forceinline__ double exp64(double x, const double *coef) {
     x = fmin(fmax(x, -1000.0), 1000.0);
@@ -258,7 +275,8 @@ __device__ __forceinline__ int group_shift(int groups) {
     return groups > 1 ? __builtin_clz((unsigned)groups - 1) - 26 : 6;
 }
 
-// The row's kept groups by binary64 choices, which are left in the wave's row of LDS.
+// The lanes of the row's kept groups by binary64 choices, which are left in the wave's row of
+// LDS.
 template <typename T, int Q, bool SIGMOID>
 __device__ __forceinline__ unsigned long long exact_groups(size_t row, float m, double *choice, const double *coef) {
     const ArgsPtr a = args_in_memory();
@@ -306,6 +324,7 @@ __device__ __forceinline__ int exact_ids(size_t row, float m, double *choice, co
     const unsigned long long kept = exact_groups<T, Q, SIGMOID>(row, m, choice, coef);
     const ArgsPtr a = args_in_memory();
     const int lane = threadIdx.x % 64, experts = a->experts, per = experts / a->groups, k = a->k;
+    const int shift = group_shift(a->groups);
     const bool by_logit = a->bias == nullptr;
 #pragma unroll 1
     for (int e0 = 0; e0 < experts; e0 += 64) {
@@ -313,7 +332,7 @@ __device__ __forceinline__ int exact_ids(size_t row, float m, double *choice, co
         double c = choice[e];
         // without a bias the order within the kept groups is the logits'
         if (by_logit && c > kLow) c = (double)logit_at<T>(a->X, row * a->ldx, e, experts);
-        choice[e] = (kept >> ((e / per) & 63)) & 1 ? c : kLow;
+        choice[e] = (kept >> (((e / per) << shift) & 63)) & 1 ? c : kLow;
     }
     int id = -1;
 #pragma unroll 1
@@ -342,196 +361,298 @@ __device__ __forceinline__ int exact_ids(size_t row, float m, double *choice, co
     return id;
 }
 
-// Rows of more than 512 experts are always decided on binary64 scores: 16 keys and their lane
-// masks per lane do not fit the scalar registers.
+// Rows of more than 512 experts are always decided on binary64 scores: 16 keys per lane, and
+// the order of them, would take more registers than the rest of the kernel.
 constexpr bool has_keys(int Q) { return Q <= 8; }
 
-constexpr int kRouteWaves = 16;
-constexpr int kRouteGrid = 512;  // workgroups; each takes every kRouteGrid-th group of rows
+// Logits lane Q ... lane Q + Q - 1 of a row, -infinity past its experts.  vec: whole chunks of
+// Q, aligned to their bytes or 16.
+template <typename T, int Q>
+__device__ __forceinline__ void load_logits(const void *X, size_t x0, int lane, int experts, bool vec, float (&x)[Q]) {
+    struct alignas(Q * sizeof(T) < 16 ? Q * sizeof(T) : 16) Chunk {
+        T v[Q];
+    };
+    if (vec) {
+        const Chunk c = *(const Chunk *)((const T *)X + x0 + min(lane * Q, experts - Q));
+#pragma unroll
+        for (int q = 0; q < Q; ++q) x[q] = lane * Q < experts ? to_float(c.v[q]) : -__builtin_huge_valf();
+    } else {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) x[q] = logit_at<T>(X, x0, lane * Q + q, experts);
+    }
+}
 
-// BIAS: choices add a.bias.  GROUPS: a.top_groups < a.groups.  SINGLE: one workgroup takes
-// every row, and writes the counts; else they are added to.
+// A lane's keys in descending order, equal ones by expert; returns (four bits each, the first
+// key's lowest) which of the lane's experts they are: a bitonic network of compare-exchanges
+// on 64-bit pairs of key and the expert's place from the lane's end.
+template <int Q>
+__device__ __forceinline__ uint32_t sort_keys(uint32_t (&key)[Q]) {
+    unsigned long long p[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) p[q] = (unsigned long long)key[q] << 32 | (unsigned)(Q - 1 - q);
+#pragma unroll
+    for (int size = 2; size <= Q; size *= 2)
+#pragma unroll
+        for (int d = size / 2; d > 0; d /= 2)
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (!(q & d)) {
+                    const unsigned long long a = p[q], b = p[q | d];
+                    const bool swap = (q & size) ? a > b : a < b;
+                    p[q] = swap ? b : a;
+                    p[q | d] = swap ? a : b;
+                }
+    uint32_t order = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        key[q] = (uint32_t)(p[q] >> 32);
+        order |= (Q - 1 - (uint32_t)p[q]) << 4 * q;
+    }
+    return order;
+}
+
+// Waves of a workgroup that takes every row, with at most half a CU's LDS.
+constexpr int route_waves(int experts) { return experts <= 256 ? 16 : experts <= 512 ? 8 : 4; }
+// Workgroups of 4 waves at most.  With 1024 the full call above takes 27.7 against 26.7 us,
+// counts included, the one without groups and bias 15.6 against 13.6.
+constexpr int kRouteGrid = 2048;
+
+// The ids of a row: place i in lane i, -1 for none.  m: softmax's maximum; bad: no routing
+// (NaN, for softmax +infinity).  b, top_b: the lane's biases and a bound of all; group_at: the
+// first lane of each expert's group; choice: the wave's row of LDS.
 template <typename T, int Q, bool SIGMOID, bool BIAS, bool GROUPS>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a, bool renorm, bool single) {
+__device__ __forceinline__ int choose(const RouteArgs &a, size_t row, bool vec, const float (&b)[Q], float top_b,
+                                      const int (&group_at)[Q], int per, double *choice, const double *coef, float &m,
+                                      bool &bad) {
+    constexpr float kNegInf = -__builtin_huge_valf();
+    // the lane as each row's own value, or the masks of absent experts, two scalar registers
+    // each, are kept across rows
+    int lane = threadIdx.x % 64;
+    asm volatile("" : "+v"(lane));
+    float x[Q];
+    load_logits<T, Q>(a.X, row * a.ldx, lane, a.experts, vec, x);
+    m = kNegInf;
+    bad = false;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        bad |= __builtin_amdgcn_classf(x[q], SIGMOID ? 0x003 : 0x203);   // NaN, +infinity
+        m = fmaxf(m, x[q]);
+    }
+    bad = __any(bad);
+    if constexpr (!SIGMOID) m = wave_max(m);
+    if (bad || (!SIGMOID && !(m > kNegInf))) return -1;
+    int id = -1;
+    bool near = true;
+    if constexpr (has_keys(Q)) {
+        // binary32 scores s, each within 2^-24 (1 + (E / 64 + 32) s) of the exact one: a
+        // score's relative error is at most 2^-24 (2 |x| + 8), for softmax 2^-24 (2 |x - m|
+        // + E / 64 + 32) with the sum's, and 2 d exp(-d) < 1
+        uint32_t key[Q];
+        float s[Q];
+        float margin = 0.0f;
+        if constexpr (BIAS || GROUPS) {
+            float largest = 1.0f;
+            if constexpr (SIGMOID) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[q]));
+            } else {
+                float sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    s[q] = __expf(x[q] - m);
+                    sum += s[q];
+                }
+                largest = 1.0f / wave_allreduce_sum(sum);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) s[q] *= largest;
+            }
+            // two choices' errors, with the sum's with the bias
+            margin = 2.0f * 0x1p-24f * (1.0f + (Q + 34.0f) * largest + 2.0f * top_b);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if constexpr (BIAS) s[q] += b[q];
+            const float c = BIAS ? s[q] : x[q];
+            const bool out = !(x[q] > kNegInf) || (BIAS && !(c > kNegInf));
+            key[q] = out ? 0u : key_of(c);
+            if constexpr (GROUPS) s[q] = out ? kNegInf : s[q];
+        }
+        near = false;
+        if constexpr (GROUPS) {
+            const ArgsPtr am = args_in_memory();
+            const int groups = am->groups, shift = group_shift(groups), S = 1 << shift;
+            float score;
+            if (per == Q << shift) {   // a group's experts are those of its own lanes
+                float best = s[0], second = kNegInf;
+#pragma unroll
+                for (int q = 1; q < Q; ++q) merge_two(best, second, s[q], kNegInf);
+                score = group_score(best, second, S, am->group_top);
+            } else {
+                float *c = (float *)choice;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) c[lane * Q + q] = s[q];
+                wave_lds_sync();
+                score = group_score((const float *)c + min(lane >> shift, groups - 1) * per, per, S, lane & (S - 1),
+                                    am->group_top);
+                wave_lds_sync();
+            }
+            bool close;
+            unsigned long long kept = best_groups(score, groups, am->top_groups, shift, 2.5f * margin, close);
+            if (close) kept = exact_groups<T, Q, SIGMOID>(row, m, choice, coef);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) key[q] = (kept >> group_at[q]) & 1 ? key[q] : 0u;
+        }
+        // The places, the i-th key in lane i as its id.  Each lane's first key is the largest
+        // it has left; the lowest lane that holds the wave's largest is taken, and its next
+        // key moves up.  With a bias, one more place to see how far the last is from what
+        // stays out: neighbours closer than the margin are put in order in binary64, and if
+        // the one after the last is as close to the next, the row is left to binary64 choices
+        // altogether.
+        uint32_t order = sort_keys(key);
+        uint32_t my_key = 0;
+        const int places = BIAS ? min(a.k + 1, 64) : a.k;
+        for (int i = 0; i < places; ++i) {
+            const uint32_t v = wave_max_u32(key[0]);
+            if (v == 0) break;
+            const int from = __builtin_ctzll(__ballot(key[0] == v));
+            const int at = from * Q + (__builtin_amdgcn_readlane(order, from) & 15);
+            const bool here = lane == i;
+            id = here ? at : id;
+            if constexpr (BIAS) my_key = here ? v : my_key;
+            const bool taken = lane == from;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) key[q] = !taken ? key[q] : q + 1 < Q ? key[q + 1 < Q ? q + 1 : q] : 0u;
+            order = taken ? order >> 4 : order;
+        }
+        if constexpr (BIAS) {
+            const uint32_t after = __shfl_down(my_key, 1, 64);
+            const bool close = lane < 63 && after != 0 && of_key(my_key) - of_key(after) <= margin;
+            const unsigned long long w = __ballot(close);   // lane i: places i and i + 1
+            if (w != 0) {
+                bool lost = places == 64;   // no lane for the one after the last
+                if (!lost && ((w >> (places - 2)) & 1)) {
+                    const uint32_t last = __builtin_amdgcn_readlane(my_key, places - 1);
+                    const uint32_t v = wave_max_u32(key[0]);
+                    lost = v != 0 && of_key(last) - of_key(v) <= margin;
+                }
+                near = lost;
+                if (!lost) id = exact_order<T, SIGMOID>(row, m, id, coef);
+            }
+            id = lane < a.k ? id : -1;
+        }
+    }
+    if constexpr (BIAS || GROUPS || !has_keys(Q))
+        if (near) id = exact_ids<T, Q, SIGMOID>(row, m, choice, coef);
+    return id;
+}
+
+// BIAS: choices add a.bias.  GROUPS: a.top_groups < a.groups.  vec: load_logits.  A wave
+// chooses for two rows one after the other (one where k > 32), and finds the weights of both
+// at once, a place per lane.  single: one workgroup takes every row and writes the counts;
+// else they are set to zero here, for route_count_kernel.
+template <typename T, int Q, bool SIGMOID, bool BIAS, bool GROUPS>
+__global__ __launch_bounds__(1024) void route_kernel(RouteArgs a, bool renorm, bool single, bool vec) {
     constexpr bool kExact = BIAS || GROUPS || !has_keys(Q);
-    __shared__ double choice_lds[kExact ? kRouteWaves : 1][kExact ? Q * 64 : 1];
+    extern __shared__ double choice_lds[];   // kExact: Q * 64 per wave
     __shared__ int hist[Q * 64];
     __shared__ double coef[kTaylor];
-    const int wave = threadIdx.x / 64, lane0 = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane0 = threadIdx.x % 64;
+    const int waves = blockDim.x / 64;
     constexpr float kNegInf = -__builtin_huge_valf();
-    const bool count = a.counts != nullptr;
+    const bool count = a.counts != nullptr && single;
     taylor_to_lds(coef);
     if (count)
-        for (int e = threadIdx.x; e < a.experts; e += 64 * kRouteWaves) hist[e] = 0;
+        for (int e = threadIdx.x; e < a.experts; e += blockDim.x) hist[e] = 0;
+    if (a.counts != nullptr && !single && blockIdx.x == 0)
+        for (int e = threadIdx.x; e < a.experts; e += blockDim.x) a.counts[e] = 0;
     __syncthreads();
     float b[Q], top_b = 0.0f;
     if constexpr (BIAS && has_keys(Q)) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const int e = q * 64 + lane0;
+            const int e = lane0 * Q + q;
             b[q] = e < a.experts ? a.bias[e] : 0.0f;
             // a masked expert's bias bounds nothing (NaN: the maximum ignores it)
             top_b = fmaxf(top_b, b[q] == kNegInf ? 0.0f : fabsf(b[q]));
         }
         top_b = wave_max(top_b);
     }
-    int per = 1, group_of[Q];   // of an absent expert, whose key is 0: any group
+    int per = 1, group_at[Q];   // of an absent expert, whose key is 0: any lane
     if constexpr (GROUPS && has_keys(Q)) {
         per = a.experts / a.groups;
+        // e / per for e below 1024: e + 1/2 is 1 / (2 per) off any multiple, far above the rounding
+        const float inv = 1.0f / (float)per;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) group_of[q] = ((q * 64 + lane0) / per) & 63;
+        for (int q = 0; q < Q; ++q)
+            group_at[q] = ((int)(((float)(lane0 * Q + q) + 0.5f) * inv) << group_shift(a.groups)) & 63;
     }
-    for (int row = blockIdx.x * kRouteWaves + wave; row < a.rows; row += gridDim.x * kRouteWaves) {
-        // the lane as each row's own value, or the masks of absent experts, two scalar registers
-        // each, are kept across rows
-        int lane = lane0;
-        asm volatile("" : "+v"(lane));
-        float x[Q], m = kNegInf;
-        bool bad = false;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            x[q] = logit_at<T>(a.X, (size_t)row * a.ldx, q * 64 + lane, a.experts);
-            // NaN, and for softmax +infinity
-            bad |= __builtin_amdgcn_classf(x[q], SIGMOID ? 0x003 : 0x203);
-            m = fmaxf(m, x[q]);
-        }
-        bad = __any(bad);
-        if constexpr (!SIGMOID) m = wave_max(m);
+    const int span = a.k <= 32 ? 32 : 64;   // lanes of a row's places
+    const int half = lane0 / span, slot = lane0 & (span - 1);
+    const int stride = gridDim.x * waves;
+    for (int first = blockIdx.x * waves + wave; first < a.rows; first += stride * (64 / span)) {
         int id = -1;
-        if (!bad && (SIGMOID || m > kNegInf)) {
-            bool near = true;
-            if constexpr (has_keys(Q)) {
-                // binary32 scores s, each within 2^-24 (1 + (E / 64 + 32) s) of the exact one: a
-                // score's relative error is at most 2^-24 (2 |x| + 8), for softmax 2^-24 (2 |x - m|
-                // + E / 64 + 32) with the sum's, and 2 d exp(-d) < 1
-                uint32_t key[Q];
-                float s[Q];
-                float margin = 0.0f;
-                if constexpr (BIAS || GROUPS) {
-                    float largest = 1.0f;
-                    if constexpr (SIGMOID) {
-#pragma unroll
-                        for (int q = 0; q < Q; ++q) s[q] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[q]));
-                    } else {
-                        float sum = 0.0f;
-#pragma unroll
-                        for (int q = 0; q < Q; ++q) {
-                            s[q] = __expf(x[q] - m);
-                            sum += s[q];
-                        }
-                        largest = 1.0f / wave_allreduce_sum(sum);
-#pragma unroll
-                        for (int q = 0; q < Q; ++q) s[q] *= largest;
-                    }
-                    // two choices' errors, with the sum's with the bias
-                    margin = 2.0f * 0x1p-24f * (1.0f + (Q + 34.0f) * largest + 2.0f * top_b);
-                }
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    if constexpr (BIAS) s[q] += b[q];
-                    const float c = BIAS ? s[q] : x[q];
-                    const bool out = !(x[q] > kNegInf) || (BIAS && !(c > kNegInf));
-                    key[q] = out ? 0u : key_of(c);
-                    if constexpr (GROUPS) s[q] = out ? kNegInf : s[q];
-                }
-                near = false;
-                if constexpr (GROUPS) {
-                    const ArgsPtr am = args_in_memory();
-                    const int groups = am->groups;
-                    float *choice = (float *)choice_lds[wave];
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) choice[q * 64 + lane] = s[q];
-                    wave_lds_sync();
-                    const int shift = group_shift(groups);
-                    const int mine = min(lane >> shift, groups - 1);
-                    const float score = group_score((const float *)choice + mine * per, per, 1 << shift,
-                                                    lane & ((1 << shift) - 1), am->group_top);
-                    wave_lds_sync();
-                    bool close;
-                    unsigned long long kept = best_groups(score, groups, am->top_groups, shift, 2.5f * margin, close);
-                    if (close) kept = exact_groups<T, Q, SIGMOID>(row, m, choice_lds[wave], coef);
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) key[q] = (kept >> group_of[q]) & 1 ? key[q] : 0u;
-                }
-                // The places, the i-th key in lane i as its id.  With a bias, one more to see
-                // how far the last is from what stays out: neighbours closer than the margin
-                // are put in order in binary64, and if the one after the last is as close to
-                // the next, the row is left to binary64 choices altogether.
-                uint32_t my_key = 0, v = 0;
-                const auto next = [&]() {
-                    v = key[0];
-#pragma unroll
-                    for (int q = 1; q < Q; ++q) v = max(v, key[q]);
-                    v = wave_max_u32(v);
-                };
-                const int places = BIAS ? min(a.k + 1, 64) : a.k;
-                for (int i = 0; i < places; ++i) {
-                    next();
-                    if (v == 0) break;
-                    int at = 0;
-#pragma unroll
-                    for (int q = Q - 1; q >= 0; --q) {
-                        const unsigned long long w = __ballot(key[q] == v);
-                        at = w != 0 ? q * 64 + __builtin_ctzll(w) : at;
-                    }
-                    const bool here = lane == i;
-                    id = here ? at : id;
-                    if constexpr (BIAS) my_key = here ? v : my_key;
-#pragma unroll
-                    for (int q = 0; q < Q; ++q)
-                        if (at >> 6 == q) key[q] = lane == (at & 63) ? 0u : key[q];   // one q: a scalar branch
-                }
-                if constexpr (BIAS) {
-                    const uint32_t after = __shfl_down(my_key, 1, 64);
-                    const bool close = lane < 63 && after != 0 && of_key(my_key) - of_key(after) <= margin;
-                    const unsigned long long w = __ballot(close);   // lane i: places i and i + 1
-                    if (w != 0) {
-                        bool lost = places == 64;   // no lane for the one after the last
-                        if (!lost && ((w >> (places - 2)) & 1)) {
-                            const uint32_t last = __builtin_amdgcn_readlane(my_key, places - 1);
-                            next();
-                            lost = v != 0 && of_key(last) - of_key(v) <= margin;
-                        }
-                        near = lost;
-                        if (!lost) id = exact_order<T, SIGMOID>(row, m, id, coef);
-                    }
-                    id = lane < a.k ? id : -1;
-                }
-            }
-            if constexpr (kExact)
-                if (near) id = exact_ids<T, Q, SIGMOID>(row, m, choice_lds[wave], coef);
-        }
-        // the weights, in binary64: place i in lane i
-        const float xi = id >= 0 ? logit_at<T>(a.X, (size_t)row * a.ldx, id, a.experts) : kNegInf;
-        double w = score64<SIGMOID>(xi, m, coef);
-        if (renorm) {
-            const double total = lanes_sum64(w, a.k <= 8 ? 8 : 64);
-            w = total > 0.0 ? w / total : 0.0;
-        } else if constexpr (!SIGMOID) {
-            double sum = 0.0;
+        float m = kNegInf;
+        bool bad = false;
+        double sum = 1.0;
 #pragma unroll 1
-            for (int e0 = 0; e0 < a.experts; e0 += 64)
-                sum += score64<false>(logit_at<T>(a.X, (size_t)row * a.ldx, e0 + lane, a.experts), m, coef);
-            sum = wave_sum64(sum);
-            w = sum > 0.0 ? w / sum : 0.0;
+        for (int h = 0; h < 64 / span; ++h) {
+            const int row = first + h * stride;
+            if (row >= args_in_memory()->rows) break;
+            float m_h;
+            bool bad_h;
+            int id_h = choose<T, Q, SIGMOID, BIAS, GROUPS>(a, row, vec, b, top_b, group_at, per,
+                                                           choice_lds + wave * (Q * 64), coef, m_h, bad_h);
+            if (h > 0) id_h = __shfl(id_h, slot, 64);
+            double sum_h = 1.0;
+            if (!SIGMOID && !renorm) sum_h = divisor64<T, SIGMOID>(a.X, (size_t)row * a.ldx, a.experts, m_h, coef);
+            id = half == h ? id_h : id;
+            m = half == h ? m_h : m;
+            bad = half == h ? bad_h : bad;
+            sum = half == h ? sum_h : sum;
         }
+        // the weights, in binary64
         const ArgsPtr am = args_in_memory();
+        const int row = first + half * stride;
+        const float xi = id >= 0 ? logit_at<T>(am->X, (size_t)row * am->ldx, id, am->experts) : kNegInf;
+        double w = score64<SIGMOID>(xi, m, coef);
+        if (renorm) sum = lanes_sum64(w, am->k <= 8 ? 8 : span);
+        w = sum > 0.0 ? w / sum : 0.0;
         w *= (double)am->scale;
         if (id < 0) w = bad ? __builtin_nan("") : 0.0;
-        if (lane < a.k) {
-            am->ids[(size_t)row * a.k + lane] = id;
-            am->weights[(size_t)row * a.k + lane] = (float)w;
+        if (slot < am->k && row < am->rows) {
+            am->ids[(size_t)row * am->k + slot] = id;
+            am->weights[(size_t)row * am->k + slot] = (float)w;
             if (count && id >= 0) atomicAdd(&hist[id], 1);
         }
     }
     if (!count) return;
     __syncthreads();
     int32_t *counts = args_in_memory()->counts;
-    for (int e = threadIdx.x; e < a.experts; e += 64 * kRouteWaves) {
-        const int n = hist[e];
-        if (single) counts[e] = n;
-        else if (n > 0) atomicAdd(counts + e, n);
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) counts[e] = hist[e];
+}
+
+// counts (zeros before) += how often each expert is among the n ids.  Per workgroup in LDS, then
+// added in memory: whole numbers, so in any order.
+constexpr int kCountGrid = 256, kCountIds = 4096;  // workgroups at most, ids of one at least
+__global__ __launch_bounds__(1024) void route_count_kernel(size_t n, int experts, const int32_t *__restrict__ ids,
+                                                           int32_t *counts) {
+    __shared__ int hist[kMaxExperts];
+    for (int e = threadIdx.x; e < experts; e += 1024) hist[e] = 0;
+    __syncthreads();
+    for (size_t i0 = (size_t)blockIdx.x * kCountIds; i0 < n; i0 += (size_t)gridDim.x * kCountIds) {
+        int id[kCountIds / 1024];
+#pragma unroll
+        for (int j = 0; j < kCountIds / 1024; ++j) {
+            const size_t i = i0 + j * 1024 + threadIdx.x;
+            id[j] = i < n ? ids[i] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kCountIds / 1024; ++j)
+            if (id[j] >= 0) atomicAdd(&hist[id[j]], 1);
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += 1024)
+        if (hist[e] > 0) atomicAdd(counts + e, hist[e]);
 }
 
 // Sums and maxima over aligned runs of n lanes, n a power of two; in every lane.
@@ -741,22 +862,24 @@ gemm355_status gemm355_route(int dtype, unsigned flags, int rows, int experts, i
     }
     if (rows == 0 && counts == nullptr) return GEMM355_OK;
     if (!current_device_is_gfx950()) return GEMM355_ERR_DEVICE;
-    const bool single = rows > 0 && rows <= kRouteWaves;  // one workgroup writes the counts itself
-    if (counts != nullptr && !single) {
+    const bool single = rows > 0 && rows <= route_waves(experts);  // one workgroup writes the counts itself
+    if (rows == 0) {
         hipLaunchKernelGGL(zero_counts_kernel, dim3(cdiv(experts, 256)), dim3(256), 0, stream, experts, counts);
-        if (hipGetLastError() != hipSuccess) return GEMM355_ERR_LAUNCH;
+        return hipGetLastError() == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH;
     }
-    if (rows == 0) return GEMM355_OK;
     const RouteArgs a{rows, experts, k, groups, top_groups, group_top, X, ldx, bias, scale, ids, weights, counts};
     const bool renorm = flags & GEMM355_ROUTE_RENORM;
-    const dim3 grid(cdiv(rows, kRouteWaves) < kRouteGrid ? cdiv(rows, kRouteWaves) : kRouteGrid), block(64 * kRouteWaves);
-    const hipError_t e = by_type_and_width(dtype, experts, [&](auto t, auto q) {
+    const int waves = single ? route_waves(experts) : 4;
+    const dim3 grid(std::min(cdiv(rows, waves), kRouteGrid)), block(64 * waves);
+    hipError_t e = by_type_and_width(dtype, experts, [&](auto t, auto q) -> hipError_t {
         using T = decltype(t);
         constexpr int Q = decltype(q)::value;
+        const bool vec = experts % Q == 0 && ldx % Q == 0 && (uintptr_t)X % (Q * es < 16 ? Q * es : 16) == 0;
         const auto go = [&](auto sig, auto has_bias, auto in_groups) {
+            constexpr bool exact = decltype(has_bias)::value || decltype(in_groups)::value || !has_keys(Q);
             hipLaunchKernelGGL((route_kernel<T, Q, decltype(sig)::value, decltype(has_bias)::value,
                                              decltype(in_groups)::value>),
-                               grid, block, 0, stream, a, renorm, single);
+                               grid, block, exact ? waves * Q * 512 : 0, stream, a, renorm, single, vec);
         };
         const auto with = [&](auto sig, auto has_bias) {
             top_groups < groups ? go(sig, has_bias, std::true_type{}) : go(sig, has_bias, std::false_type{});
@@ -767,6 +890,12 @@ gemm355_status gemm355_route(int dtype, unsigned flags, int rows, int experts, i
             bias != nullptr ? with(std::false_type{}, std::true_type{}) : with(std::false_type{}, std::false_type{});
         return hipGetLastError();
     });
+    if (e == hipSuccess && counts != nullptr && !single) {
+        const size_t n = (size_t)rows * k, parts = (n + kCountIds - 1) / kCountIds;
+        hipLaunchKernelGGL(route_count_kernel, dim3(parts < kCountGrid ? parts : kCountGrid), dim3(1024), 0, stream, n,
+                           experts, ids, counts);
+        e = hipGetLastError();
+    }
     return e == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH;
 }
 

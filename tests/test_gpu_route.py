@@ -151,6 +151,23 @@ def test_route_choices_a_rounding_apart(kind, E):
     check_route(X, "f32", 8, kind=kind, groups=4, top_groups=1, group_top=1)
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(32, 8), (20, 3), (48, 33), (64, 32)])
+def test_route_many_rows(E, k, kind):
+    """More rows than the grid has waves: a wave takes two rows at once (one for k > 32), either
+    of which may have nothing to choose."""
+    rows = 8192 + 2600
+    X = ref.make_router(rows, E, "f32", 3)
+    X[5] = -np.inf                       # the first of a wave's two
+    X[8192 + 6] = -np.inf                # the second
+    X[[7, 8192 + 7, 8192 + 8], [1, 2, 3]] = np.nan
+    X[9, 2:] = -np.inf                   # fewer than k left
+    X[8192 + 10, 2:] = -np.inf
+    bias = np.random.default_rng(E).standard_normal(E) * 0.1
+    check_route(X, "f32", k, kind=kind)
+    check_route(X, "f32", k, kind=kind, bias=bias, renorm=True, pad=1)
+
+
 def test_route_chosen_scores_of_zero():
     # the bias chooses experts whose softmax is 0 in binary64 (800 below the maximum)
     X = np.full((2, 32), -800.0, np.float32)

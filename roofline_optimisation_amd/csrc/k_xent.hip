@@ -494,7 +494,7 @@ int even_pieces(int N, long fit) {
 }
 
 struct FusedForwardPlan {
-    int rows, cols, blocks, Kp, ldw;
+    int rows, cols, Kp, ldw;
     float2 *part;
     float *zl;
     uint16_t *Xm, *Wm;
@@ -505,18 +505,24 @@ struct FusedForwardPlan {
         Kp = padded_hidden(K);
         cols = copied ? even_pieces(N, kCopyBytes / 2 / Kp) : N;
         ldw = flags & GEMM355_TRANS_B ? Kp : (int)up((size_t)cols, 8);
-        blocks = 0;
-        for (int v0 = 0; v0 < N; v0 += cols) {
-            Section part[2];
-            const int n = head_sections(rows, N - v0 < cols ? N - v0 : cols, Kp, part);
-            for (int i = 0; i < n; ++i) blocks += stat_blocks(part[i]);
-        }
+        // the last rows may take smaller tiles, and so more blocks, than the others
+        const int rest = M % rows;
         Carver c{(char *)ws};
-        part = (float2 *)c.take((size_t)blocks * rows * sizeof(float2));
+        part = (float2 *)c.take(std::max(pairs(rows, N), rest > 0 ? pairs(rest, N) : 0) * sizeof(float2));
         zl = (float *)c.take((size_t)rows * 4);
         Xm = (uint16_t *)c.take((size_t)rows * Kp * 2);
         Wm = (uint16_t *)c.take(copied ? (size_t)(flags & GEMM355_TRANS_B ? cols : Kp) * ldw * 2 : 0);
         bytes = c.used;
+    }
+    // the (maximum, sum) pairs of n rows
+    size_t pairs(int n, int N) const {
+        size_t blocks = 0;
+        for (int v0 = 0; v0 < N; v0 += cols) {
+            Section part[2];
+            const int sections = head_sections(n, N - v0 < cols ? N - v0 : cols, Kp, part);
+            for (int i = 0; i < sections; ++i) blocks += stat_blocks(part[i]);
+        }
+        return blocks * n;
     }
 };
 
@@ -671,13 +677,13 @@ gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, con
                 const HeadArgs h{rows, c.cols, p.Kp, copy_x ? p.Xm : x, copy_x ? p.Kp : ldx,
                                  at(w, w_offset(flags, c.v0, lw), 2), lw, tb};
                 G355_TRY(dtype == kF16
-                             ? launch_xent_stats_f16(c.tile, h, labels + r0, v0 + c.v0, part, p.rows, p.zl, s)
-                             : launch_xent_stats_bf16(c.tile, h, labels + r0, v0 + c.v0, part, p.rows, p.zl, s));
-                part += (size_t)stat_blocks(c) * p.rows;
+                             ? launch_xent_stats_f16(c.tile, h, labels + r0, v0 + c.v0, part, rows, p.zl, s)
+                             : launch_xent_stats_bf16(c.tile, h, labels + r0, v0 + c.v0, part, rows, p.zl, s));
+                part += (size_t)stat_blocks(c) * rows;
                 blocks += stat_blocks(c);
             }
         }
-        G355_TRY(merge(rows, N, blocks, p.part, p.rows, p.zl, labels + r0, ignore, loss ? loss + r0 : nullptr,
+        G355_TRY(merge(rows, N, blocks, p.part, rows, p.zl, labels + r0, ignore, loss ? loss + r0 : nullptr,
                        lse ? lse + r0 : nullptr, s));
     }
     return GEMM355_OK;

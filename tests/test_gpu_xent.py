@@ -340,6 +340,15 @@ def test_many_rows_of_few_classes(M, N, K, dtype, trans_b):
     check_grad(h, lse, upstream(M, 1, dtype), (M, N, K), padx=1, padw=2)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rest,N,K", [(500, 1000, 256), (20, 300, 264), (1, 256, 128), (3000, 1000, 260)])
+def test_rows_past_a_block_of_rows(rest, N, K, dtype):
+    """The loss takes 32768 rows at a time; the few after them may take smaller tiles, with more
+    statistics a row."""
+    X, W, y = ref.make_head(32768 + rest, N, K, dtype, rest)
+    check_xent(Head(X, W, y, dtype, True), (rest, N, K))
+
+
 def test_repeated_calls_give_the_same_bits():
     for dtype in ("f32", "bf16"):
         X, W, y = ref.make_head(200, 3001, 256, dtype, 14)

@@ -920,32 +920,42 @@ gemm355_status gemm355_route_grad(int dtype, unsigned flags, int rows, int exper
         return GEMM355_ERR_INVALID_ARG;
     if (!current_device_is_gfx950()) return GEMM355_ERR_DEVICE;
     const bool renorm = flags & GEMM355_ROUTE_RENORM, sigmoid = flags & GEMM355_ROUTE_SIGMOID;
-    hipError_t e;
-    if (sigmoid || renorm) {
-        int n = 1;
-        while (n < k) n *= 2;
-        const int fit = kGradLds / experts, R = fit < 64 / n ? fit : 64 / n;
-        const bool vec = experts % 4 == 0 && lddx % 4 == 0 && (uintptr_t)dX % (4 * es) == 0;
-        const dim3 grid(cdiv(rows, 4 * R));
-        e = by_type(dtype, [&](auto t) {
-            using T = decltype(t);
-            const auto go = [&](auto sig, auto v) {
-                hipLaunchKernelGGL((route_grad_chosen_kernel<T, decltype(sig)::value, decltype(v)::value>), grid,
-                                   dim3(256), 0, stream, rows, experts, k, X, ldx, ids, dweights, scale, dX, lddx,
-                                   renorm, n, R);
-            };
-            if (sigmoid) vec ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
-            else vec ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
-            return hipGetLastError();
-        });
-    } else {
-        e = by_type_and_width(dtype, experts, [&](auto t, auto q) {
-            hipLaunchKernelGGL((route_grad_kernel<decltype(t), decltype(q)::value>), dim3(cdiv(rows, 4)), dim3(256), 0,
-                               stream, rows, experts, k, X, ldx, ids, dweights, scale, dX, lddx);
-            return hipGetLastError();
-        });
+    // rows of one launch: its threads (64 a row at most) number fewer than 2^32
+    constexpr int kRows = 1 << 25;
+    for (int r0 = 0; r0 < rows; r0 += kRows) {
+        const int live = std::min(rows - r0, kRows);
+        const char *x = (const char *)X + (size_t)r0 * ldx * es;
+        char *dx = (char *)dX + (size_t)r0 * lddx * es;
+        const int32_t *id = ids + (size_t)r0 * k;
+        const float *dw = dweights + (size_t)r0 * k;
+        hipError_t e;
+        if (sigmoid || renorm) {
+            int n = 1;
+            while (n < k) n *= 2;
+            const int fit = kGradLds / experts, R = fit < 64 / n ? fit : 64 / n;
+            const bool vec = experts % 4 == 0 && lddx % 4 == 0 && (uintptr_t)dX % (4 * es) == 0;
+            const dim3 grid(cdiv(live, 4 * R));
+            e = by_type(dtype, [&](auto t) {
+                using T = decltype(t);
+                const auto go = [&](auto sig, auto v) {
+                    hipLaunchKernelGGL((route_grad_chosen_kernel<T, decltype(sig)::value, decltype(v)::value>), grid,
+                                       dim3(256), 0, stream, live, experts, k, x, ldx, id, dw, scale, dx, lddx, renorm,
+                                       n, R);
+                };
+                if (sigmoid) vec ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+                else vec ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+                return hipGetLastError();
+            });
+        } else {
+            e = by_type_and_width(dtype, experts, [&](auto t, auto q) {
+                hipLaunchKernelGGL((route_grad_kernel<decltype(t), decltype(q)::value>), dim3(cdiv(live, 4)), dim3(256),
+                                   0, stream, live, experts, k, x, ldx, id, dw, scale, dx, lddx);
+                return hipGetLastError();
+            });
+        }
+        if (e != hipSuccess) return GEMM355_ERR_LAUNCH;
     }
-    return e == hipSuccess ? GEMM355_OK : GEMM355_ERR_LAUNCH;
+    return GEMM355_OK;
 }
 
 }  // extern "C"

@@ -499,11 +499,12 @@ struct FusedForwardPlan {
     float *zl;
     uint16_t *Xm, *Wm;
     size_t bytes;
-    // copied: W is copied, `cols` classes at a time
+    // `cols` classes at a time, which keep a launch's threads below 2^32, or, where W is copied,
+    // the copy to kCopyBytes
     FusedForwardPlan(bool copied, unsigned flags, int M, int N, int K, void *ws) {
         rows = M < kStatRows ? M : kStatRows;
         Kp = padded_hidden(K);
-        cols = copied ? even_pieces(N, kCopyBytes / 2 / Kp) : N;
+        cols = even_pieces(N, copied ? kCopyBytes / 2 / Kp : 1L << 22);
         ldw = flags & GEMM355_TRANS_B ? Kp : (int)up((size_t)cols, 8);
         // the last rows may take smaller tiles, and so more blocks, than the others
         const int rest = M % rows;

@@ -246,3 +246,39 @@ def test_route_grad_odd_ids(kind, renorm):
     dw = np.random.default_rng(2).standard_normal(ids.shape).astype(np.float32)
     check_grad(X, "f32", ids, dw, "odd ids", kind=kind, renorm=renorm)
     check_grad(X, "f32", ids, dw, "odd ids in place", kind=kind, renorm=renorm, in_place=True, pad=2)
+
+
+def test_more_rows_than_a_launch_has_threads_for():
+    """2^26 rows and more: 64 threads a row would be 2^32."""
+    import torch
+    rows = (1 << 26) + 5
+    X = torch.randint(-4, 5, (rows, 2), device="cuda").to(torch.bfloat16)
+    ids, w, counts = gb.route(X, 1, score="sigmoid")
+    want = (X[:, 1] > X[:, 0]).to(torch.int32)
+    assert torch.equal(ids[:, 0], want)
+    ones = int(want.sum(dtype=torch.int64))
+    assert counts.tolist() == [rows - ones, ones]
+    del want
+    s = torch.sigmoid(torch.maximum(X[:, 0], X[:, 1]).float())
+    assert ((w[:, 0] - s).abs() <= 2.0 ** -20).all()
+    dX = gb.route_grad(X, ids, w, score="sigmoid")
+    chosen = torch.gather(dX, 1, ids.long())[:, 0].float()
+    # one rounding to bfloat16, and binary32's own
+    assert ((chosen - w[:, 0] * s * (1 - s)).abs() <= 2.0 ** -8 * chosen.abs() + 2.0 ** -20).all()
+    assert not torch.gather(dX, 1, 1 - ids.long()).any()
+    dX = gb.route_grad(X, ids, w, score="softmax")
+    assert torch.equal(dX[-3:], gb.route_grad(X[-3:], ids[-3:], w[-3:], score="softmax"))
+
+
+def test_infinite_bias():
+    """A bias of +infinity chooses its expert first, of several the lowest; with NaN or -infinity
+    an expert is out."""
+    bias = np.zeros(40)
+    bias[[7, 30]] = np.inf
+    bias[9] = -np.inf
+    bias[12] = np.nan
+    X = ref.make_router(12, 40, "f32", 3)
+    X[3, 7] = -np.inf
+    for kind in ("softmax", "sigmoid"):
+        for kw in ({}, dict(groups=5, top_groups=2, group_top=2), dict(groups=5, top_groups=3, group_top=1)):
+            check_route(X, "f32", 6, kind=kind, bias=bias, renorm=True, **kw)

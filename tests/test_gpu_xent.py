@@ -349,6 +349,28 @@ def test_rows_past_a_block_of_rows(rest, N, K, dtype):
     check_xent(Head(X, W, y, dtype, True), (rest, N, K))
 
 
+@pytest.mark.parametrize("trans_b", [True, False])
+def test_more_classes_than_a_launch_takes(trans_b):
+    """The loss takes 2^22 classes at a time."""
+    import torch
+    M, N, K = 70, (1 << 22) + 1000, 136
+    torch.manual_seed(1)
+    X = torch.randn(M, K, device="cuda").half()
+    W = (torch.randn(N, K, device="cuda") / K ** 0.5).half()
+    y = torch.randint(0, N, (M,), device="cuda")
+    y[:3] = torch.tensor([N - 1, 1 << 22, (1 << 22) - 1])
+    loss, lse = gb.linear_cross_entropy(X, W if trans_b else W.t().contiguous(), y, trans_b=trans_b)
+    Z = torch.cat([X.double() @ W[v:v + (1 << 18)].double().t() for v in range(0, N, 1 << 18)], 1)
+    want = torch.logsumexp(Z, 1)
+    # the sum's own error and a logit's, K rounded additions of products at most 2^-24 each of
+    # sum |x w| <= |x| |w|
+    size = X.double().norm(dim=1) * float(W.float().norm(dim=1).max())
+    tol = 2.0 ** -24 * (4 * want.abs() + N / 256 + 64 + K * size)
+    assert ((lse - want).abs() <= tol).all()
+    zl = Z.gather(1, y[:, None])[:, 0]
+    assert ((loss - (want - zl)).abs() <= tol + 2.0 ** -24 * (K * size + want.abs() + zl.abs())).all()
+
+
 def test_repeated_calls_give_the_same_bits():
     for dtype in ("f32", "bf16"):
         X, W, y = ref.make_head(200, 3001, 256, dtype, 14)

@@ -115,7 +115,8 @@ size_t gemm355_xent_grad_workspace(int dtype, unsigned flags, int M, int N, int 
  * nothing outside them is written.  The logits are computed again piece by piece of the
  * vocabulary and each piece of dZ is rounded to `dtype` for the two products that read it
  * (for binary16 after scaling by the power of two that puts the largest |dloss_t| in
- * [2^13, 2^14), so that small probabilities are not lost); the products are summed in
+ * [2^13, 2^14), so that small probabilities are not lost; up to 64 rows and with 256
+ * classes or more, what the rounding leaves is multiplied too); the products are summed in
  * binary32 and rounded once.  Values X holds in rows without a label do not reach dW.
  * M == 0 writes dW = 0. */
 gemm355_status gemm355_xent_grad(int dtype, unsigned flags, int M, int N, int K, const void *X,

@@ -330,11 +330,28 @@ int piece_cols(int M, int N) {
     return (int)(c < all ? c : all);
 }
 
+// The ranges of `step` terms that a binary32 product of M x cols is summed over: four
+// workgroups a CU where its 64 x 64 tiles number fewer than `few`, each of 256 terms or more.
+// One range: an ordinary product.
+struct F32Ranges {
+    int count = 1, step = 0;
+    F32Ranges(int few, int M, int cols, int n) {
+        const long tiles = (long)cdiv(M, 64) * cdiv(cols, 64);
+        if (tiles >= few || n < 512) return;
+        step = (int)up((size_t)std::max(cdiv(n, (int)(1024 / tiles)), 256), 32);
+        count = cdiv(n, step);
+    }
+    size_t bytes(int M, int cols) const { return count > 1 ? (size_t)count * M * cols * 4 : 0; }
+};
+
+constexpr int kFewLogits = 512, kFewDx = 256;   // F32Ranges' few
+
 constexpr int kRowBlock = 8192;  // rows whose logits are held at once in the forward pass
 
 struct ForwardPlan {
     int rows, cols, blocks, ldm;
-    float *Z, *zl;
+    F32Ranges ranges{0, 1, 1, 0};   // of the logits' sums
+    float *Z, *zl, *sums;
     float2 *part;
     void *Xm;
     size_t bytes;
@@ -350,14 +367,17 @@ struct ForwardPlan {
         part = (float2 *)c.take((size_t)blocks * rows * sizeof(float2));
         zl = (float *)c.take((size_t)rows * 4);
         Xm = c.take((size_t)rows * ldm * es);
+        const int nc = cols < N ? cols : N;
+        if (dtype == kF32) ranges = F32Ranges(kFewLogits, rows, nc, K);
+        sums = (float *)c.take(ranges.bytes(rows, nc));
         bytes = c.used;
     }
 };
 
 struct GradPlan {
     int Mp, cols, ldm;  // Mp: rows, with those of zeros that make dW's sum whole k-steps
-    int ranges, step;   // ranges of `step` classes dX is summed over; 0: one product
-    float *scale, *Z, *dX, *dW;
+    F32Ranges zr{0, 1, 1, 0}, dxr{0, 1, 1, 0};   // of the logits' and dX's sums
+    float *scale, *Z, *sums, *dX, *dW;
     RowGrad *rows;
     void *Xm, *dZ;
     size_t bytes;
@@ -369,15 +389,10 @@ struct GradPlan {
         Mp = h16 || M <= 64 ? M : (int)up((size_t)M, 32);
         cols = piece_cols(Mp, N);
         ldm = (int)up((size_t)(K > 0 ? K : 1), 16 / es);
-        ranges = step = 0;
-        // binary32 dX of fewer 64 x 64 tiles than CUs: four workgroups a CU, ranges of 256
-        // classes or more (16-bit types come here with fewer classes than that)
-        const long tiles = (long)cdiv(M, 64) * cdiv(K > 0 ? K : 1, 64);
         const int nc = cols < N ? cols : N;
-        if (!h16 && tiles < 256 && nc >= 512) {
-            const int want = (int)(1024 / tiles);
-            step = (int)up((size_t)std::max(cdiv(nc, want), 256), 32);
-            ranges = cdiv(nc, step);
+        if (!h16) {
+            zr = F32Ranges(kFewLogits, Mp, nc, K);
+            dxr = F32Ranges(kFewDx, M, K, nc);
         }
         Carver c{(char *)ws};
         scale = (float *)c.take(8);
@@ -385,7 +400,8 @@ struct GradPlan {
         Xm = c.take((size_t)Mp * ldm * es);
         Z = (float *)c.take((size_t)Mp * cols * 4);
         dZ = h16 ? c.take((size_t)Mp * cols * 2) : Z;
-        dX = h16 || ranges > 0 ? (float *)c.take((size_t)std::max(ranges, 1) * M * K * 4) : nullptr;
+        sums = (float *)c.take(zr.bytes(Mp, nc));
+        dX = (float *)c.take(h16 ? (size_t)M * K * 4 : dxr.bytes(M, K));
         dW = h16 ? (float *)c.take((size_t)cols * K * 4) : nullptr;
         bytes = c.used;
     }
@@ -653,6 +669,14 @@ hipError_t copy_weights(unsigned flags, int nc, int K, int Kp, const void *w, in
     return copy_rows(K, Kp, nc, w, ldw, Wm, ldm, s);
 }
 
+gemm355_status sum_ranges(const F32Ranges &ranges, const float *sums, int M, int cols, float *out, int ldo,
+                          hipStream_t s) {
+    return status_of(over_rows(M, [&](int r, int n) {
+        hipLaunchKernelGGL(xent_sum_kernel, dim3(cdiv(cols, 256), n), dim3(256), 0, s, cols, sums + (size_t)r * cols,
+                           ranges.count, (size_t)M * cols, out + (size_t)r * ldo, ldo);
+    }));
+}
+
 gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
                              int ldw, const int64_t *labels, int64_t ignore, float *loss, float *lse, void *ws,
                              hipStream_t s) {
@@ -690,6 +714,16 @@ gemm355_status forward_fused(int dtype, unsigned flags, int M, int N, int K, con
     return GEMM355_OK;
 }
 
+// The logits of a piece, in ranges of the hidden size or as one product.
+gemm355_status piece_logits(int dtype, unsigned flags, const F32Ranges &ranges, float *sums, int M, int nc, int K,
+                            const void *X, int ldx, const void *w, int ldw, float *Z, int ldz, hipStream_t s) {
+    if (ranges.count == 1)
+        return gemm355_gemm_ex(GEMM355_VARIANT_AUTO, dtype, flags, M, nc, K, X, ldx, w, ldw, Z, ldz, s);
+    const F32SplitArgs q{M, nc, K, (const float *)X, ldx, (const float *)w, ldw, sums, ranges.step, 0};
+    G355_TRY(launch_xent_split_f32(!(flags & GEMM355_TRANS_B), q, s));
+    return sum_ranges(ranges, sums, M, nc, Z, ldz, s);
+}
+
 gemm355_status forward(int dtype, unsigned flags, int M, int N, int K, const void *X, int ldx, const void *W,
                        int ldw, const int64_t *labels, int64_t ignore, float *loss, float *lse, void *ws,
                        hipStream_t s) {
@@ -707,8 +741,8 @@ gemm355_status forward(int dtype, unsigned flags, int M, int N, int K, const voi
         for (int v0 = 0; v0 < N; v0 += p.cols) {
             const int nc = N - v0 < p.cols ? N - v0 : p.cols;
             const gemm355_status st =
-                gemm355_gemm_ex(GEMM355_VARIANT_AUTO, dtype, flags, rows, nc, K, copy_x ? p.Xm : x,
-                                copy_x ? p.ldm : ldx, at(W, w_offset(flags, v0, ldw), es), ldw, p.Z, p.cols, s);
+                piece_logits(dtype, flags, p.ranges, p.sums, rows, nc, K, copy_x ? p.Xm : x, copy_x ? p.ldm : ldx,
+                             at(W, w_offset(flags, v0, ldw), es), ldw, p.Z, p.cols, s);
             if (st != GEMM355_OK) return st;
             hipLaunchKernelGGL(xent_chunk_kernel, dim3(cdiv(nc, kChunk), rows), dim3(256), 0, s, nc, v0, p.Z, p.cols,
                                labels + r0, p.part + (size_t)blocks * p.rows, p.rows, p.zl);
@@ -894,14 +928,14 @@ gemm355_status gradient(const GradCall &a, void *ws) {
     for (int v0 = 0; v0 < a.N; v0 += p.cols) {
         const int nc = a.N - v0 < p.cols ? a.N - v0 : p.cols;
         const char *w = at(a.W, w_offset(a.flags, v0, a.ldw), es);
-        gemm355_status st = gemm355_gemm_ex(GEMM355_VARIANT_AUTO, a.dtype, a.flags, p.Mp, nc, a.K, p.Xm, p.ldm, w,
-                                            a.ldw, p.Z, p.cols, a.s);
+        gemm355_status st = piece_logits(a.dtype, a.flags, p.zr, p.sums, p.Mp, nc, a.K, p.Xm, p.ldm, w, a.ldw, p.Z,
+                                         p.cols, a.s);
         if (st != GEMM355_OK) return st;
         e = piece_dz(a, p, v0, nc);
         if (e != hipSuccess) return status_of(e);
-        if (a.dX != nullptr && p.ranges > 0) {
-            const F32SplitArgs q{a.M, a.K, nc, p.Z, p.cols, (const float *)w, a.ldw, p.dX, p.step, v0 > 0};
-            G355_TRY(launch_xent_dx_f32(tb, q, a.s));
+        if (a.dX != nullptr && p.dxr.count > 1) {
+            const F32SplitArgs q{a.M, a.K, nc, p.Z, p.cols, (const float *)w, a.ldw, p.dX, p.dxr.step, v0 > 0};
+            G355_TRY(launch_xent_split_f32(tb, q, a.s));
         } else if (a.dX != nullptr) {
             // whole k-steps, then the rest of the classes added: with a number of classes that is
             // no multiple of 4 every load of the one product would be predicated (binary32 2048
@@ -933,11 +967,7 @@ gemm355_status gradient(const GradCall &a, void *ws) {
             }
         }
     }
-    if (p.ranges > 0 && a.dX != nullptr)
-        return status_of(over_rows(a.M, [&](int r, int n) {
-            hipLaunchKernelGGL(xent_sum_kernel, dim3(cdiv(a.K, 256), n), dim3(256), 0, a.s, a.K, p.dX + (size_t)r * a.K,
-                               p.ranges, (size_t)a.M * a.K, (float *)a.dX + (size_t)r * a.lddx, a.lddx);
-        }));
+    if (a.dX != nullptr && p.dxr.count > 1) return sum_ranges(p.dxr, p.dX, a.M, a.K, (float *)a.dX, a.lddx, a.s);
     if (h16 && a.dX != nullptr) return status_of(round16(a, a.M, a.K, p.dX, a.K, 1, 0, 0, p.scale, a.dX, a.lddx));
     return GEMM355_OK;
 }

@@ -80,18 +80,18 @@ hipError_t launch_xent_dx_bf16(int tile, bool b_mn, const ProductArgs &p, hipStr
 hipError_t launch_xent_dw_f16(int tile, const ProductArgs &p, hipStream_t s);
 hipError_t launch_xent_dw_bf16(int tile, const ProductArgs &p, hipStream_t s);
 
-// dX's product in binary32 over ranges of `step` classes (a multiple of 32): range r's sums,
-// M x K, at part + r M K, added to what is there when `add`.  dZ (M x nc, row stride ldz) has
-// rows on 16-byte boundaries; W as in HeadArgs, without its conditions.
+// A binary32 product of few tiles summed over ranges of `step` (a multiple of 32) of its n
+// terms: M x cols = A.B, range r's sums at part + r M cols, added to what is there when `add`.
+// A (M x n, row stride lda) has rows on 16-byte boundaries; B is n x cols (rows), or cols x n.
 struct F32SplitArgs {
-    int M, K, nc;
-    const float *dZ;
-    int ldz;
-    const float *W;
-    int ldw;
+    int M, cols, n;
+    const float *A;
+    int lda;
+    const float *B;
+    int ldb;
     float *part;
     int step, add;
 };
-hipError_t launch_xent_dx_f32(bool trans_b, const F32SplitArgs &p, hipStream_t s);
+hipError_t launch_xent_split_f32(bool rows, const F32SplitArgs &p, hipStream_t s);
 
 }  // namespace g355

@@ -331,26 +331,27 @@ int piece_cols(int M, int N) {
 }
 
 // The ranges of `step` terms that a binary32 product of M x cols is summed over: four
-// workgroups a CU where its 64 x 64 tiles number fewer than `few`, each of 256 terms or more.
-// One range: an ordinary product.
+// workgroups a CU where there are fewer than 512 tiles of 64 x 64, each of 256 terms or more.
+// One range: an ordinary product.  Logits of 5 x 11952 x 3973 (187 tiles) as one product 134
+// us, in 5 ranges 80 with their sum; of 8 x 91440 x 1344 (1429 tiles) the whole loss 153 as
+// one, 185 in 2; of 863 x 1152 x 1728 (252 tiles) 55 in 4, 61 in 7.  With dX, from the logits
+// on: 300 x 20000 x 4096 (320 tiles) 1058 as one, 941 in 3; 512 x 8000 x 2048 267 and 273.
 struct F32Ranges {
     int count = 1, step = 0;
-    F32Ranges(int few, int M, int cols, int n) {
+    F32Ranges(int M, int cols, int n) {
         const long tiles = (long)cdiv(M, 64) * cdiv(cols, 64);
-        if (tiles >= few || n < 512) return;
+        if (tiles >= 512 || n < 512) return;
         step = (int)up((size_t)std::max(cdiv(n, (int)(1024 / tiles)), 256), 32);
         count = cdiv(n, step);
     }
     size_t bytes(int M, int cols) const { return count > 1 ? (size_t)count * M * cols * 4 : 0; }
 };
 
-constexpr int kFewLogits = 512, kFewDx = 256;   // F32Ranges' few
-
 constexpr int kRowBlock = 8192;  // rows whose logits are held at once in the forward pass
 
 struct ForwardPlan {
     int rows, cols, blocks, ldm;
-    F32Ranges ranges{0, 1, 1, 0};   // of the logits' sums
+    F32Ranges ranges{1, 1, 0};   // of the logits' sums
     float *Z, *zl, *sums;
     float2 *part;
     void *Xm;
@@ -368,7 +369,7 @@ struct ForwardPlan {
         zl = (float *)c.take((size_t)rows * 4);
         Xm = c.take((size_t)rows * ldm * es);
         const int nc = cols < N ? cols : N;
-        if (dtype == kF32) ranges = F32Ranges(kFewLogits, rows, nc, K);
+        if (dtype == kF32) ranges = F32Ranges(rows, nc, K);
         sums = (float *)c.take(ranges.bytes(rows, nc));
         bytes = c.used;
     }
@@ -376,7 +377,7 @@ struct ForwardPlan {
 
 struct GradPlan {
     int Mp, cols, ldm;  // Mp: rows, with those of zeros that make dW's sum whole k-steps
-    F32Ranges zr{0, 1, 1, 0}, dxr{0, 1, 1, 0};   // of the logits' and dX's sums
+    F32Ranges zr{1, 1, 0}, dxr{1, 1, 0};   // of the logits' and dX's sums
     float *scale, *Z, *sums, *dX, *dW;
     RowGrad *rows;
     void *Xm, *dZ;
@@ -391,8 +392,8 @@ struct GradPlan {
         ldm = (int)up((size_t)(K > 0 ? K : 1), 16 / es);
         const int nc = cols < N ? cols : N;
         if (!h16) {
-            zr = F32Ranges(kFewLogits, Mp, nc, K);
-            dxr = F32Ranges(kFewDx, M, K, nc);
+            zr = F32Ranges(Mp, nc, K);
+            dxr = F32Ranges(M, K, nc);
         }
         Carver c{(char *)ws};
         scale = (float *)c.take(8);

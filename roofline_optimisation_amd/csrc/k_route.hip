@@ -15,13 +15,13 @@
 // largest first key (four register exchanges within 16 lanes, a scalar maximum of four lanes)
 // and the lowest lane that holds it (a ballot), whose next key moves up.
 //
-// Bound by instructions, of which the vector and the scalar unit take about as many (binary64
-// throughout: four times as many).  16384 rows of 256 experts in groups with a bias and 8
-// places take 24.4 us, their counts 3.9 more; 10 us without groups and bias, where reading the
-// logits alone would take 4.  With rounds that look through all of a lane's keys, groups
-// ranked one after the other, the weights of one row at a time and counts added up by each
-// workgroup's atomics it was 36.  Registers (88) leave five waves on a SIMD; a bound of six
-// makes the compiler spill.
+// Bound by vector instructions, 530 a row of 256 experts in groups with a bias and 8
+// places (binary64 throughout: four times as many).  16384 such rows take 22.2 us and their
+// counts 3.9 more, a call 24.3 us and without groups and bias 11.6; reading the logits alone
+// would take 4.  With rounds that look through all of a lane's keys, groups ranked one after
+// the other, the weights of one row at a time and counts added up by each workgroup's atomics
+// it was 36.  Registers (88) leave five waves on a SIMD; a bound of six makes the compiler
+// spill.
 #include <algorithm>
 
 #include "../../include/gemm355_softmax.h"
@@ -189,9 +189,9 @@ __device__ __forceinline__ unsigned long long best_groups(F score, int groups, i
     for (int g0 = 0; g0 < groups; g0 += S) {
         const int g = g0 + (lane & (S - 1));
         const F o = __shfl(score, (g << shift) & 63, 64);
-        const bool ahead = g < groups && (o > score || (o == score && g < mine));
+        const bool ahead = (g < groups) & ((o > score) | ((o == score) & (g < mine)));   // no branches
         rank += __builtin_popcount((uint32_t)(__ballot(ahead) >> first) & group_lanes);
-        close += __builtin_popcount((uint32_t)(__ballot(ahead && o - score <= margin) >> first) & group_lanes);
+        close += __builtin_popcount((uint32_t)(__ballot(ahead & (o - score <= margin)) >> first) & group_lanes);
     }
     // not kept, and one that is (ranks below top) among those just ahead
     near = __any(mine < groups && rank >= top && rank - close < top);
@@ -413,8 +413,8 @@ __device__ __forceinline__ uint32_t sort_keys(uint32_t (&key)[Q]) {
 
 // Waves of a workgroup that takes every row, with at most half a CU's LDS.
 constexpr int route_waves(int experts) { return experts <= 256 ? 16 : experts <= 512 ? 8 : 4; }
-// Workgroups of 4 waves at most.  With 1024 the full call above takes 27.7 against 26.7 us,
-// counts included, the one without groups and bias 15.6 against 13.6.
+// Workgroups of 4 waves at most.  With 1024 the two calls above take 24.4 and 13.5 us, with
+// 4096, where 16384 rows leave no wave a second one, 26.0 and 12.7.
 constexpr int kRouteGrid = 2048;
 
 // The ids of a row: place i in lane i, -1 for none.  m: softmax's maximum; bad: no routing
@@ -521,7 +521,13 @@ __device__ __forceinline__ int choose(const RouteArgs &a, size_t row, bool vec, 
             if constexpr (BIAS) my_key = here ? v : my_key;
             const bool taken = lane == from;
 #pragma unroll
-            for (int q = 0; q < Q; ++q) key[q] = !taken ? key[q] : q + 1 < Q ? key[q + 1 < Q ? q + 1 : q] : 0u;
+            for (int q = 0; q < Q; ++q) {
+                // values, not elements: a choice between elements becomes one of their index
+                const uint32_t held = key[q];
+                uint32_t after = 0;
+                if (q + 1 < Q) after = key[q + 1 < Q ? q + 1 : q];
+                key[q] = taken ? after : held;
+            }
             order = taken ? order >> 4 : order;
         }
         if constexpr (BIAS) {

@@ -64,7 +64,7 @@ constexpr int kChunk = 4096;  // columns of a row that one workgroup takes the s
 
 // The statistics of columns [4096 b, + 4096) of row r of a piece Z, workgroup (b, r), to
 // part[b * ldp + r]; zl[r] = the label's logit where it is one of them (the piece starts at
-// class v0).
+// class v0).  Bound by reading the logits: 1000 x 32000 28.9 us, 4.4 TB/s.
 __global__ __launch_bounds__(256) void xent_chunk_kernel(int nc, int v0, const float *__restrict__ Z, int ldz,
                                                          const int64_t *__restrict__ labels, float2 *part, int ldp,
                                                          float *zl) {
@@ -105,7 +105,8 @@ __global__ __launch_bounds__(256) void xent_chunk_kernel(int nc, int v0, const f
 
 // The statistics of the tiles or chunks: `blocks` pairs per row (part[block * ldp + row]) merged,
 // and the row's results written.  A workgroup takes R rows, 1024 / R threads a row: each
-// merges every (1024 / R)-th block, then the threads' pairs are merged in halves.
+// merges every (1024 / R)-th block, then the threads' pairs are merged in halves.  8192 rows of
+// 1024 pairs 13.4 us (67 MB, 5 TB/s); 16 rows of 1000 with R = 4 3.9 us, mostly the launch.
 template <int R>
 __global__ __launch_bounds__(1024) void xent_merge_kernel(int M, int N, int blocks, const float2 *__restrict__ part,
                                                           int ldp, const float *__restrict__ zl,
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(256) void xent_copy_kernel(int rows, int cols, cons
 // products with a zero row of dZ would not be zero where X holds an infinity or NaN).
 // Every workgroup finds the same maximum over all rows, then does its share of the rows.
 // Rows from M to Mp are rows without a label; with `again`, rows from `again` on are the
-// first ones' X again.
+// first ones' X again.  512 x 1024 5.0 us, the launch and two reads that wait for each other.
 template <typename E>
 __global__ __launch_bounds__(256) void xent_prep_kernel(int M, int Mp, int again, int N, int K, const E *__restrict__ X, int ldx,
                                                         const int64_t *__restrict__ labels, int64_t ignore,
@@ -237,7 +238,8 @@ __global__ __launch_bounds__(256) void xent_dz_kernel(int nc, int v0, const floa
 
 // out = scale[1] * (the sum of `splits` partial sums, `stride` apart, and with `other` of those
 // that many elements further on), rounded to the 16-bit type; four columns per thread (VEC:
-// loaded in one access; wide: stored in one).  Grid: (columns / 1024, rows).
+// loaded in one access; wide: stored in one).  Grid: (columns / 1024, rows).  8192 x 4096 from
+// one sum 34 us, 5.9 TB/s; 512 x 1024 from 16 6.6 us.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void xent_round_kernel(int cols, const float *__restrict__ acc, int lda,
                                                          int splits, size_t stride, size_t other,

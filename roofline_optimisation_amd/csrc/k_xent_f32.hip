@@ -1,7 +1,9 @@
 // Binary32 products of a head whose tiles leave CUs idle (dX of few rows, logits of few rows
 // or classes): the sum is split into ranges, one workgroup of the FP32 tile routine
 // (f32_gemm.hpp) per tile and range, and the ranges' partial sums are added afterwards.  As one
-// product, dX of 16 rows of 704 over 53476 classes runs on 11 CUs.
+// product, dX of 16 rows of 704 over 53476 classes runs on 11 CUs.  With few
+// rows it reads W, at 2.6 TB/s where W's rows are not 16-byte aligned (dX of 5 x 11952 x 3973 73
+// us) and 3.4 where they are (5 x 82770 x 1984 196 us).
 #include "f32_gemm.hpp"
 #include "xent.hpp"
 

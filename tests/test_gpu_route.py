@@ -60,6 +60,8 @@ def run_route(X, dtype, k, kind="softmax", bias=None, groups=1, top_groups=1, gr
 
 def check_route(X, dtype, k, **kw):
     pad = kw.pop("pad", 0)
+    if kw.get("bias") is not None:
+        kw["bias"] = kw["bias"].astype(np.float32)   # the plain form adds what the kernel is given
     ids, w, n = run_route(X, dtype, k, pad=pad, **kw)
     rids, rw, rn = ref.route(X, dtype, k, **{**kw, "scale": float(np.float32(kw.get("scale", 1.0)))})
     assert np.array_equal(ids, rids), np.argwhere(ids != rids)[:4]

@@ -7,8 +7,8 @@
 // tiles, us per tile, 94 of it the sum alone): statistics 99.5, of which a quarter is the
 // exponentials (256 per lane at a quarter of the vector rate); dZ 105, whose stores leave
 // from all CUs at once (33.5 MB a round); dW 89 (a sum over 8192 rows, per 4096 of them).
-// Whole passes: 8192 x 131072 x 4096 statistics 6.2-6.4 ms (1.38-1.42 PFLOP/s), dZ 4 x 1.68,
-// dX 4 x 1.51, dW 4 x 1.42 ms; the same product alone in the vendor's library 5.8-6.2 ms.
+// Whole passes: 8192 x 131072 x 4096 statistics 6.2-6.4 ms (1.38-1.42 PFLOP/s), dZ 4 x 1.68-1.74,
+// dX 4 x 1.49-1.55, dW 4 x 1.42-1.46 ms; the same product alone in the vendor's library 5.8-6.2 ms.
 #pragma once
 
 #include "h16_gemm.hpp"
